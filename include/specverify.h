@@ -85,6 +85,7 @@ typedef enum {
 #define SPEC_DEV_BAD_LENGTH 0x2u  /* L + k + 1 exceeds the sequence's block-table row */
 #define SPEC_DEV_TIMEOUT 0x4u     /* a bounded mbarrier wait gave up */
 #define SPEC_DEV_BAD_TOKEN 0x8u   /* a token id outside [0, vocab) */
+#define SPEC_DEV_NONFINITE 0x10u  /* an infinity or NaN among rows to be stored in 8 bits */
 
 /* Limits of this implementation. */
 #define SPEC_MAX_K 16             /* drafts per step, k in [0, 16] */
@@ -344,6 +345,162 @@ int spec_draft(const spec_model* m, const spec_drafter* d, const int32_t* block_
                const int32_t* seq_lens, const void* prev_hidden, const int32_t* prev_token, int B,
                int k, int32_t* drafts, float* draft_maxlogit, void* ws, size_t ws_bytes,
                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions in their general form.  The pages give p-RoPE only ("Gemma
+ * 4 拆解" §2: a fraction of the pairs turns); contexts longer than the trained
+ * one and the other pair layout need the rest.
+ *
+ * Pair j < n_rot of each head takes dims (j, j + span/2) (HALF) or (2j, 2j + 1)
+ * (INTERLEAVED); every other dim passes through unchanged.  At position t, with
+ * c = magnitude * cos(t f_j) and s = magnitude * sin(t f_j):
+ *   y0 = x0 c - x1 s,   y1 = x0 s + x1 c.
+ * Frequencies, with b = theta, g_j = b^(-2j/span) and S = factor:
+ *   PLAIN   f_j = g_j
+ *   LINEAR  f_j = g_j / S                 (positions compressed by S)
+ *   RAISED  b := b * S^(span/(span-2)), f_j = g_j   (the slowest pair slows by S)
+ *   PARTS   r_j = original * g_j / (2 pi) turns over the original length;
+ *           w = clamp((r_j - turns_lo) / (turns_hi - turns_lo), 0, 1);
+ *           f_j = (1 - w) g_j / S + w g_j  (fast pairs kept, slow ones compressed;
+ *           Peng et al., "YaRN", 2023, section 3.2; magnitude is its attention
+ *           temperature's square root, 0.1 ln S + 1 there)
+ * p-RoPE is HALF, span = head_dim, n_rot = p * head_dim / 2, PLAIN.
+ * ------------------------------------------------------------------------- */
+#define SPEC_ROPE_HALF 0
+#define SPEC_ROPE_INTERLEAVED 1
+#define SPEC_ROPE_PLAIN 0
+#define SPEC_ROPE_LINEAR 1
+#define SPEC_ROPE_RAISED 2
+#define SPEC_ROPE_PARTS 3
+#define SPEC_BF16 0
+#define SPEC_FP16 1
+#define SPEC_FP32 2
+#define SPEC_ROPE_MAX_DIM 256     /* head_dim limit of spec_rope */
+
+typedef struct spec_rope_config {
+  int layout;          /* SPEC_ROPE_HALF / SPEC_ROPE_INTERLEAVED */
+  int span;            /* dims the pairs are laid over: even, 2..head_dim (RAISED: >= 4) */
+  int n_rot;           /* turned pairs, 0..span/2 */
+  int scaling;         /* SPEC_ROPE_PLAIN .. SPEC_ROPE_PARTS */
+  double theta;        /* base, > 0 */
+  double factor;       /* S >= 1 (PLAIN: ignored) */
+  double original;     /* PARTS: the original length, > 0 */
+  double turns_lo;     /* PARTS: 0 <= turns_lo < turns_hi */
+  double turns_hi;
+  double magnitude;    /* > 0, multiplies cos and sin */
+} spec_rope_config;
+
+/* Host: the n_rot frequencies f_j (binary64).  out: host array, n_rot long. */
+int spec_rope_frequencies(const spec_rope_config* r, int head_dim, double* out);
+
+/* Turns the heads of n_rows rows: x and out [n_rows][n_heads][head_dim] of dtype
+ * (SPEC_BF16 / SPEC_FP16 / SPEC_FP32), the dims of a head next to each other,
+ * row and head strides in elements (out: heads and rows must not overlap; x may
+ * repeat, stride 0).  positions [n_rows] int32 (device); a row whose position is
+ * negative is a padding row: its out is left as it was.  inverse != 0 turns
+ * back (the transpose: also the gradient of x given that of out).  out may be x
+ * with the same strides; otherwise the two must not overlap.  Angles are formed
+ * in binary64, products and sums in binary32, results rounded once.
+ * head_dim 2..SPEC_ROPE_MAX_DIM; pointers aligned to their element type. */
+int spec_rope(const spec_rope_config* r, int dtype, const void* x, int64_t x_row_stride,
+              int64_t x_head_stride, void* out, int64_t out_row_stride, int64_t out_head_stride,
+              const int32_t* positions, int n_rows, int n_heads, int head_dim, int inverse,
+              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged KV cache held in 8 bits.  Keys (turned) and values are stored as e4m3
+ * codes (1 sign, 4 exponent, 3 fraction bits, largest 448, no infinities) with
+ * one binary32 scale per (block of block_tokens tokens of a page, KV head), one
+ * for keys and one for values: the entry stands for code * scale.  Half the
+ * bytes of the bf16 pools, of which the verify step reads every one.
+ *
+ * spec_qcache_write chooses powers of two: the least 2^e with
+ * amax <= 448 * 2^e, e in [-100, 100] (2^-100 for a block of zeros; magnitudes
+ * above 448 * 2^100 become that).  A code is the nearest e4m3 value, ties to
+ * even, of the exactly scaled entry.  Where a block already holds committed
+ * tokens (positions below seq_lens[b]) it keeps the larger of its scale and the
+ * new rows'; if its scale rises the committed codes are rewritten for it, which
+ * is exact except for codes that fall below e4m3's normal range, since the ratio
+ * is a power of two.  So drafts that are rolled back cost a block no more than
+ * that.  Infinities and NaN among the rows set SPEC_DEV_NONFINITE; they do not
+ * enter the scale, an infinity is stored as the largest code, NaN as 0: pages
+ * hold finite numbers only, so a masked entry cannot reach a result.
+ * Pools filled by other means may carry any finite scale in [2^-100, 2^100]
+ * (zero too, for a block of zeros).
+ *
+ * Layouts, 16-byte aligned:
+ *   k_pool, v_pool   [num_pages][n_kv_heads][page_size][head_dim] e4m3
+ *   k_scale, v_scale [num_pages][n_kv_heads][page_size / block_tokens] binary32
+ * Key-equals-value layers store their values (the pre-RoPE keys) in v_pool.
+ * ------------------------------------------------------------------------- */
+typedef struct spec_qcache {
+  int head_dim;          /* 128 or 256 */
+  int n_kv_heads;
+  int num_pages;
+  int page_size;         /* SPEC_PAGE_SIZE */
+  int block_tokens;      /* tokens a scale covers: 16, 32 or 64 */
+  int split_tokens;      /* split-KV chunk of the attention: a multiple of 128 up to 4096, 0 = 1024;
+                            results depend on it, not on the batch or the rows of a call */
+  void* k_pool;
+  void* v_pool;
+  void* k_scale;
+  void* v_scale;
+} spec_qcache;
+
+#define SPEC_QCACHE_MAX_WRITE 65536   /* new tokens per sequence of one write */
+
+/* Workspace bytes of spec_qcache_write (0 on invalid arguments). */
+size_t spec_qcache_write_workspace_bytes(const spec_qcache* c, int max_batch, int max_n);
+
+/* Stores n new tokens per sequence at positions seq_lens[b] .. seq_lens[b]+n-1
+ * (seq_lens is not changed: the caller commits).
+ *   k_new, v_new: bf16, row b*n + i at row_stride elements (a multiple of 8,
+ *   >= n_kv_heads * head_dim), [n_kv_heads][head_dim] in a row; keys are turned
+ *   by r at their positions first (r NULL: stored as given).
+ *   block_table [B][max_pages], seq_lens [B] int32.
+ * A sequence that does not fit its block-table row (or a negative length) sets
+ * SPEC_DEV_BAD_LENGTH and is skipped; a page id outside the pool sets
+ * SPEC_DEV_BAD_PAGE and that block is skipped.  No two sequences may write the
+ * same page in one call.  n = 0 is valid and does nothing. */
+int spec_qcache_write(const spec_qcache* c, const spec_rope_config* r, const int32_t* block_table,
+                      int max_pages, const int32_t* seq_lens, int B, int n, const void* k_new,
+                      int64_t k_row_stride, const void* v_new, int64_t v_row_stride, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* Workspace bytes of spec_qcache_attn and spec_qcache_verify_attn for batches up
+ * to max_batch, n up to max_n and block tables up to max_pages (0 on invalid
+ * arguments).  window: the window of the calls, 0 for none. */
+size_t spec_qcache_attn_workspace_bytes(const spec_qcache* c, int n_q_heads, int max_batch, int max_n,
+                                        int max_pages, int window);
+
+/* Grouped-query attention of n rows per sequence over the 8-bit cache (read
+ * only).  Row i of sequence b sits at position p = seq_lens[b] + q_offset + i and
+ * sees keys j <= p, j < seq_lens[b] + kv_extra and, with window > 0, j > p -
+ * window: a verify step or prompt chunk whose rows have been written is q_offset
+ * 0, kv_extra n; a drafter's step s over the committed cache is q_offset s,
+ * kv_extra 0.  A row that sees no key gets zeros.
+ *   q [B * n] rows at q_row_stride elements (a multiple of 8, >= n_q_heads *
+ *   head_dim), bf16, turned by r at p first (r NULL: used as given);
+ *   out [B][n][n_q_heads][head_dim] bf16; scale 0 = 1/sqrt(head_dim).
+ * n in [1, SPEC_MAX_PREFILL], q_offset and kv_extra in [0, 65536].  A query row
+ * with an infinity or NaN gives a row of NaN and touches no other.  Keys on a
+ * page id outside the pool are left out (SPEC_DEV_BAD_PAGE); a sequence whose
+ * length is negative or whose keys do not fit its block-table row gives zeros
+ * (SPEC_DEV_BAD_LENGTH).
+ * For n <= SPEC_MAX_K + 1 a row's result does not depend on n, B or its place. */
+int spec_qcache_attn(const spec_qcache* c, const spec_rope_config* r, const void* q,
+                     int64_t q_row_stride, int n_q_heads, const int32_t* block_table, int max_pages,
+                     const int32_t* seq_lens, int B, int n, int q_offset, int kv_extra, int window,
+                     float scale, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* spec_verify_attn over an 8-bit cache: spec_qcache_write of the n new rows, then
+ * spec_qcache_attn with q_offset 0 and kv_extra n, in one call. */
+int spec_qcache_verify_attn(const spec_qcache* c, const spec_rope_config* r, const void* q,
+                            int64_t q_row_stride, int n_q_heads, const void* k_new,
+                            int64_t k_row_stride, const void* v_new, int64_t v_row_stride,
+                            const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                            int B, int n, int window, float scale, void* out, void* ws,
+                            size_t ws_bytes, void* stream);
 
 /* LM head + argmax without a workspace, for callers that cannot allocate
  * device memory.  The pages have no counterpart: this is a deployment aid.

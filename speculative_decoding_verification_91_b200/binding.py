@@ -24,6 +24,7 @@ SPEC_DEV_BAD_PAGE = 0x1
 SPEC_DEV_BAD_LENGTH = 0x2
 SPEC_DEV_TIMEOUT = 0x4
 SPEC_DEV_BAD_TOKEN = 0x8
+SPEC_DEV_NONFINITE = 0x10
 SPEC_MAX_K = 16
 SPEC_PAGE_SIZE = 64
 
@@ -38,9 +39,17 @@ EXPORTED = [
     "spec_cluster_unembed_workspace_bytes", "spec_cluster_unembed",
     "spec_verify_sampled_workspace_bytes", "spec_verify_step_sampled",
     "spec_noalloc_read_status", "spec_noalloc_inject_status",
+    "spec_rope_frequencies", "spec_rope",
+    "spec_qcache_write_workspace_bytes", "spec_qcache_write",
+    "spec_qcache_attn_workspace_bytes", "spec_qcache_attn", "spec_qcache_verify_attn",
 ]
 SPEC_MAX_PREFILL = 256
 SPEC_NOALLOC_MAX_ROWS = 64
+SPEC_ROPE_HALF, SPEC_ROPE_INTERLEAVED = 0, 1
+SPEC_ROPE_PLAIN, SPEC_ROPE_LINEAR, SPEC_ROPE_RAISED, SPEC_ROPE_PARTS = 0, 1, 2, 3
+SPEC_BF16, SPEC_FP16, SPEC_FP32 = 0, 1, 2
+SPEC_ROPE_MAX_DIM = 256
+SPEC_QCACHE_MAX_WRITE = 65536
 
 
 class SpecError(RuntimeError):
@@ -83,6 +92,22 @@ class SpecDrafter(ctypes.Structure):
         ("d_draft", c_int), ("n_q_heads", c_int), ("n_blocks", c_int),
         ("w_embed", c_void_p), ("w_down", c_void_p), ("w_up", c_void_p),
         ("blocks", POINTER(SpecDraftBlock)), ("clusters", POINTER(SpecClusters)),
+    ]
+
+
+class SpecRope(ctypes.Structure):
+    _fields_ = [
+        ("layout", c_int), ("span", c_int), ("n_rot", c_int), ("scaling", c_int),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+        ("turns_lo", ctypes.c_double), ("turns_hi", ctypes.c_double), ("magnitude", ctypes.c_double),
+    ]
+
+
+class SpecQCache(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", c_int), ("n_kv_heads", c_int), ("num_pages", c_int), ("page_size", c_int),
+        ("block_tokens", c_int), ("split_tokens", c_int),
+        ("k_pool", c_void_p), ("v_pool", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
     ]
 
 
@@ -150,7 +175,23 @@ def lib():
                                                c_int, c_int, c_float, c_void_p, c_void_p, c_void_p,
                                                c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                                c_size_t, c_void_p]
-        sizes = ("spec_prefill_workspace_bytes", "spec_draft_workspace_bytes",
+        pr, pq = POINTER(SpecRope), POINTER(SpecQCache)
+        i64 = ctypes.c_int64
+        L.spec_rope_frequencies.argtypes = [pr, c_int, POINTER(ctypes.c_double)]
+        L.spec_rope.argtypes = [pr, c_int, c_void_p, i64, i64, c_void_p, i64, i64, c_void_p, c_int,
+                                c_int, c_int, c_int, c_void_p]
+        L.spec_qcache_write_workspace_bytes.argtypes = [pq, c_int, c_int]
+        L.spec_qcache_write.argtypes = [pq, pr, c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, i64,
+                                        c_void_p, i64, c_void_p, c_size_t, c_void_p]
+        L.spec_qcache_attn_workspace_bytes.argtypes = [pq, c_int, c_int, c_int, c_int, c_int]
+        L.spec_qcache_attn.argtypes = [pq, pr, c_void_p, i64, c_int, c_void_p, c_int, c_void_p, c_int,
+                                       c_int, c_int, c_int, c_int, c_float, c_void_p, c_void_p,
+                                       c_size_t, c_void_p]
+        L.spec_qcache_verify_attn.argtypes = [pq, pr, c_void_p, i64, c_int, c_void_p, i64, c_void_p, i64,
+                                              c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_float,
+                                              c_void_p, c_void_p, c_size_t, c_void_p]
+        sizes = ("spec_qcache_write_workspace_bytes", "spec_qcache_attn_workspace_bytes",
+                 "spec_prefill_workspace_bytes", "spec_draft_workspace_bytes",
                  "spec_cluster_unembed_workspace_bytes", "spec_verify_sampled_workspace_bytes")
         for name in EXPORTED[4:]:
             if name not in sizes:
@@ -351,3 +392,56 @@ def spec_verify_step_sampled(model, block_table, max_pages, last_token, drafts, 
         B, k, float(temperature), _p(u_accept), _p(u_draw), _p(seq_lens), _p(accept_len),
         _p(emitted), _p(new_last_token), _p(target_logits), _p(ws), ws_bytes, _s(stream)),
         "spec_verify_step_sampled")
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def spec_rope_frequencies(rope: SpecRope, head_dim: int) -> list:
+    """The n_rot frequencies (radians per position) of a rotary configuration."""
+    out = (ctypes.c_double * max(1, rope.n_rot))()
+    _check(lib().spec_rope_frequencies(ctypes.byref(rope), head_dim, out), "spec_rope_frequencies")
+    return list(out[:rope.n_rot])
+
+
+def spec_rope(rope, dtype, x, x_row_stride, x_head_stride, out, out_row_stride, out_head_stride,
+              positions, n_rows, n_heads, head_dim, inverse=0, stream=None) -> int:
+    return _check(lib().spec_rope(_ref(rope), dtype, _p(x), x_row_stride, x_head_stride, _p(out),
+                                  out_row_stride, out_head_stride, _p(positions), n_rows, n_heads,
+                                  head_dim, inverse, _s(stream)), "spec_rope")
+
+
+def spec_qcache_write_workspace_bytes(cache, max_batch: int, max_n: int) -> int:
+    return int(lib().spec_qcache_write_workspace_bytes(_ref(cache), max_batch, max_n))
+
+
+def spec_qcache_write(cache, rope, block_table, max_pages, seq_lens, B, n, k_new, k_row_stride, v_new,
+                      v_row_stride, ws, ws_bytes, stream=None) -> int:
+    return _check(lib().spec_qcache_write(_ref(cache), _ref(rope), _p(block_table), max_pages,
+                                          _p(seq_lens), B, n, _p(k_new), k_row_stride, _p(v_new),
+                                          v_row_stride, _p(ws), ws_bytes, _s(stream)),
+                  "spec_qcache_write")
+
+
+def spec_qcache_attn_workspace_bytes(cache, n_q_heads: int, max_batch: int, max_n: int, max_pages: int,
+                                     window: int = 0) -> int:
+    return int(lib().spec_qcache_attn_workspace_bytes(_ref(cache), n_q_heads, max_batch, max_n,
+                                                      max_pages, window))
+
+
+def spec_qcache_attn(cache, rope, q, q_row_stride, n_q_heads, block_table, max_pages, seq_lens, B, n,
+                     q_offset, kv_extra, window, scale, out, ws, ws_bytes, stream=None) -> int:
+    return _check(lib().spec_qcache_attn(_ref(cache), _ref(rope), _p(q), q_row_stride, n_q_heads,
+                                         _p(block_table), max_pages, _p(seq_lens), B, n, q_offset,
+                                         kv_extra, window, scale, _p(out), _p(ws), ws_bytes, _s(stream)),
+                  "spec_qcache_attn")
+
+
+def spec_qcache_verify_attn(cache, rope, q, q_row_stride, n_q_heads, k_new, k_row_stride, v_new,
+                            v_row_stride, block_table, max_pages, seq_lens, B, n, window, scale, out,
+                            ws, ws_bytes, stream=None) -> int:
+    return _check(lib().spec_qcache_verify_attn(
+        _ref(cache), _ref(rope), _p(q), q_row_stride, n_q_heads, _p(k_new), k_row_stride, _p(v_new),
+        v_row_stride, _p(block_table), max_pages, _p(seq_lens), B, n, window, scale, _p(out), _p(ws),
+        ws_bytes, _s(stream)), "spec_qcache_verify_attn")

@@ -1,0 +1,281 @@
+// The 8-bit paged cache: the append that quantises (spec_qcache_write), the
+// queries' form for the attention over it, and a plain attention kernel.
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "qcache.h"
+
+namespace sv {
+
+namespace {
+
+constexpr int kPg = SPEC_PAGE_SIZE;
+constexpr int kWriteThreads = 256;
+
+__device__ __forceinline__ bool finite_f(float x) { return fabsf(x) <= 3.4028234e38f; }
+
+// A binary64 value as the binary32 one next to it towards zero, its last bit
+// set when that was not exact (rounding to odd): rounding the result once more
+// to few bits then gives what rounding the binary64 value at once gives.
+__device__ __forceinline__ float to_odd(double y) {
+  const float f = __double2float_rz(y);
+  return static_cast<double>(f) == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Element d of a head of the row at p, turned by r at pos, rounded to odd.
+__device__ __forceinline__ float turned(const RopeArgs& r, const uint16_t* p, int d, int pos) {
+  const int half = r.span / 2;
+  int j = -1, e = d;          // pair and partner dim
+  bool second = false;
+  if (r.layout == SPEC_ROPE_HALF) {
+    if (d < r.n_rot) j = d, e = d + half;
+    else if (d >= half && d < half + r.n_rot) j = d - half, e = j, second = true;
+  } else if (d < 2 * r.n_rot) {
+    j = d >> 1, e = d ^ 1, second = d & 1;
+  }
+  const double x = bf16_to_f32(p[d]);
+  if (j < 0) return static_cast<float>(x);
+  const double w = bf16_to_f32(p[e]);
+  double c, s;
+  rope_turn(pos, r.turns[j], c, s);
+  c *= r.magnitude;
+  s *= r.magnitude;
+  return to_odd(second ? w * s + x * c : x * c - w * s);
+}
+
+// One CTA per (touched block of tokens, KV head, sequence), keys (z even) or
+// values (z odd).
+__global__ void __launch_bounds__(kWriteThreads) qcache_write_kernel(const __grid_constant__ RopeArgs r,
+                                                                     const __grid_constant__ QWriteArgs a) {
+  extern __shared__ float rows[];            // [block][dim]
+  __shared__ float red[kWriteThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const QCacheArgs& c = a.c;
+  const int b = blockIdx.z >> 1, is_v = blockIdx.z & 1, h = blockIdx.y;
+  const int L = c.seq_lens[b];
+  if (L < 0 || static_cast<int64_t>(L) + a.n > static_cast<int64_t>(c.max_pages) * kPg) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0) flag_status(c.status, SPEC_DEV_BAD_LENGTH);
+    return;
+  }
+  const int p0 = (L / c.block + static_cast<int>(blockIdx.x)) * c.block;   // first position of the block
+  if (p0 >= L + a.n) return;
+  const int page = c.block_table[static_cast<int64_t>(b) * c.max_pages + p0 / kPg];
+  if (page < 0 || page >= c.num_pages) {
+    if (threadIdx.x == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
+    return;
+  }
+  const int lo = max(p0, L), hi = min(p0 + c.block, L + a.n);   // new positions
+  const int D = c.dim;
+  const uint16_t* src = is_v ? a.v_new : a.k_new;
+  const int64_t stride = is_v ? a.v_row : a.k_row;
+  float amax = 0.f;
+  bool bad = false;
+  for (int i = threadIdx.x; i < (hi - lo) * D; i += kWriteThreads) {
+    const int pos = lo + i / D, d = i % D;
+    const uint16_t* p = src + (static_cast<int64_t>(b) * a.n + (pos - L)) * stride + static_cast<int64_t>(h) * D;
+    const float y = is_v ? bf16_to_f32(p[d]) : turned(r, p, d, pos);
+    rows[i] = y;
+    if (finite_f(y)) amax = fmaxf(amax, fabsf(y));
+    else bad = true;
+  }
+  if (bad) flag_status(c.status, SPEC_DEV_NONFINITE);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  for (int w = 0; w < kWriteThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+
+  const int64_t head = static_cast<int64_t>(page) * c.n_kv_heads + h;
+  float* sc = (is_v ? c.vs : c.ks) + head * (kPg / c.block) + (p0 % kPg) / c.block;
+  uint8_t* dst = (is_v ? c.v : c.k) + (head * kPg + p0 % kPg) * D;
+  float now = pow2f(scale_exponent(amax));
+  const float was = *sc;
+  if (lo > p0) {
+    now = fmaxf(now, was);
+    if (now > was) {                         // rewrite the committed codes for the larger scale
+      const float ratio = __fdiv_rn(was, now);
+      for (int i = threadIdx.x; i < (lo - p0) * D / 2; i += kWriteThreads) {
+        uint16_t* q = reinterpret_cast<uint16_t*>(dst) + i;
+        const float2 v = e4m3_values(*q);
+        *q = e4m3x2(v.x == v.x ? v.x * ratio : 0.f, v.y == v.y ? v.y * ratio : 0.f);
+      }
+    }
+  }
+  const float inv = __fdiv_rn(1.f, now);
+  for (int i = threadIdx.x; i < (hi - lo) * D / 2; i += kWriteThreads) {
+    float v[2] = {rows[2 * i], rows[2 * i + 1]};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) v[e] = v[e] == v[e] ? v[e] * inv : 0.f;
+    reinterpret_cast<uint16_t*>(dst + (lo - p0) * D)[i] = e4m3x2(v[0], v[1]);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) *sc = now;
+}
+
+// Queries: one warp per head of a row.  q = q_scale * (code0 + code1): the
+// first code keeps 4 significant bits, the second 4 of what is left, so the two
+// hold a query to 2^-9 of itself (and 2^-19 of the row's largest), finer than
+// bf16's 2^-9 on average, and both factors of the score product are e4m3.  A
+// row with an infinity or NaN gets a NaN scale, which makes its result NaN.
+__global__ void __launch_bounds__(256) qcache_query_kernel(const __grid_constant__ RopeArgs r,
+                                                           const __grid_constant__ QAttnArgs a) {
+  __shared__ float2 cs[kMaxPairs];
+  pdl_trigger();
+  pdl_wait();
+  const int i = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = a.c.dim, H = a.c.n_kv_heads;
+  const int L = a.c.seq_lens[b];
+  const int pos = min(max(L, 0), 1 << 30) + a.q_offset + i;
+  for (int j = threadIdx.x; j < r.n_rot; j += 256) {
+    double c, s;
+    rope_turn(pos, r.turns[j], c, s);
+    cs[j] = make_float2(static_cast<float>(c * r.magnitude), static_cast<float>(s * r.magnitude));
+  }
+  __syncthreads();
+  const int per = D / 32, half = r.span / 2;
+  const int64_t plane = static_cast<int64_t>(a.B) * H * a.rows * D;
+  for (int hq = warp; hq < H * a.G; hq += 8) {
+    const uint16_t* p = a.q + (static_cast<int64_t>(b) * a.n + i) * a.q_row + static_cast<int64_t>(hq) * D;
+    float y[8], amax = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e >= per) break;
+      const int d = lane * per + e;
+      int j = -1, w = d;
+      bool second = false;
+      if (r.layout == SPEC_ROPE_HALF) {
+        if (d < r.n_rot) j = d, w = d + half;
+        else if (d >= half && d < half + r.n_rot) j = d - half, w = j, second = true;
+      } else if (d < 2 * r.n_rot) {
+        j = d >> 1, w = d ^ 1, second = d & 1;
+      }
+      float x = bf16_to_f32(p[d]);
+      if (j >= 0) {
+        const float x2 = bf16_to_f32(p[w]);
+        x = second ? x2 * cs[j].y + x * cs[j].x : x * cs[j].x - x2 * cs[j].y;
+      }
+      y[e] = x;
+      if (finite_f(x)) amax = fmaxf(amax, fabsf(x));
+      else bad = true;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    bad = __any_sync(0xffffffffu, bad);
+    const int e2 = scale_exponent(amax);
+    const float inv = pow2f(-e2);
+    const int h = hq / a.G, g = hq % a.G;
+    const int64_t row = (static_cast<int64_t>(b) * H + h) * a.rows + static_cast<int64_t>(i) * a.G + g;
+    uint8_t* dst = a.q_codes + row * D + lane * per;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      if (e >= per) break;
+      const float u = bad ? 0.f : y[e] * inv, v = bad ? 0.f : y[e + 1] * inv;
+      const uint32_t c0 = e4m3x2(u, v);
+      const float2 f = e4m3_values(c0);
+      *reinterpret_cast<uint16_t*>(dst + e) = c0;
+      *reinterpret_cast<uint16_t*>(dst + plane + e) = e4m3x2(u - f.x, v - f.y);
+    }
+    if (lane == 0) a.q_scale[row] = bad ? __int_as_float(0x7fffffff) : pow2f(e2);
+  }
+}
+
+// A CTA per (row, KV head, sequence): four warps take the row's keys in turn,
+// each with its own running maximum and sums, joined at the end.
+__global__ void __launch_bounds__(128) qcache_attn_plain_kernel(const __grid_constant__ QAttnArgs a) {
+  __shared__ float o_s[4][256];
+  __shared__ float m_s[4], l_s[4];
+  pdl_trigger();
+  pdl_wait();
+  const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const QCacheArgs& c = a.c;
+  const int D = c.dim, per = D / 32, H = c.n_kv_heads;
+  const int i = r / a.G, g = r % a.G;
+  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + i) * H * a.G + h * a.G + g) * D;
+  const int L = c.seq_lens[b];
+  const bool fits = L >= 0 && static_cast<int64_t>(L) + a.kv_extra <= static_cast<int64_t>(c.max_pages) * kPg;
+  if (!fits && threadIdx.x == 0 && r == 0 && h == 0) flag_status(c.status, SPEC_DEV_BAD_LENGTH);
+  const int pos = L + a.q_offset + i;
+  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  const int hi = fits ? min(pos, L + a.kv_extra - 1) : -1;
+  const int64_t row = (static_cast<int64_t>(b) * H + h) * a.rows + r;
+  const int64_t plane = static_cast<int64_t>(a.B) * H * a.rows * D;
+  float q[8], o[8], m = -INFINITY, l = 0.f;
+  const float qsc = a.q_scale[row];
+  const float qs = qsc == qsc ? qsc * a.scale_log2 : 0.f;
+  for (int e = 0; e < 8; ++e) o[e] = q[e] = 0.f;
+  for (int e = 0; e < per; e += 2) {
+    const int64_t at = row * D + lane * per + e;
+    const float2 x = e4m3_values(*reinterpret_cast<const uint16_t*>(a.q_codes + at));
+    const float2 y = e4m3_values(*reinterpret_cast<const uint16_t*>(a.q_codes + plane + at));
+    q[e] = x.x + y.x;
+    q[e + 1] = x.y + y.y;
+  }
+  for (int j = lo + warp; j <= hi; j += 4) {
+    const int page = c.block_table[static_cast<int64_t>(b) * c.max_pages + j / kPg];
+    if (page < 0 || page >= c.num_pages) {
+      if (lane == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
+      continue;
+    }
+    const int64_t head = static_cast<int64_t>(page) * H + h;
+    const int64_t at = (head * kPg + j % kPg) * D + lane * per;
+    const int64_t sc = head * (kPg / c.block) + (j % kPg) / c.block;
+    float s = 0.f, v[8];
+    for (int e = 0; e < per; e += 2) {
+      const float2 kk = e4m3_values(*reinterpret_cast<const uint16_t*>(c.k + at + e));
+      const float2 vv = e4m3_values(*reinterpret_cast<const uint16_t*>(c.v + at + e));
+      s += q[e] * kk.x + q[e + 1] * kk.y;
+      v[e] = vv.x;
+      v[e + 1] = vv.y;
+    }
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    s *= qs * c.ks[sc];
+    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn), pv = p * c.vs[sc];
+    for (int e = 0; e < per; ++e) o[e] = o[e] * al + pv * v[e];
+    l = l * al + p;
+    m = mn;
+  }
+  for (int e = 0; e < per; ++e) o_s[warp][lane * per + e] = o[e];
+  if (lane == 0) m_s[warp] = m, l_s[warp] = l;
+  __syncthreads();
+  const float M = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+  float den = 0.f;
+  for (int w = 0; w < 4; ++w) den += m_s[w] == -INFINITY ? 0.f : l_s[w] * exp2f(m_s[w] - M);
+  for (int d = threadIdx.x; d < D; d += 128) {
+    float x = 0.f;
+    for (int w = 0; w < 4; ++w) x += m_s[w] == -INFINITY ? 0.f : o_s[w][d] * exp2f(m_s[w] - M);
+    dst[d] = den == 0.f ? 0 : f32_to_bf16(qsc == qsc ? x / den : qsc);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st) {
+  const int blocks = (a.n + a.c.block - 2) / a.c.block + 1;   // that n tokens may touch
+  const size_t smem = static_cast<size_t>(a.c.block) * a.c.dim * 4;
+  cudaError_t e = cudaFuncSetAttribute(qcache_write_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       64 * 256 * 4);
+  if (e != cudaSuccess) return e;
+  return launch_k(qcache_write_kernel, dim3(blocks, a.c.n_kv_heads, 2 * a.B), dim3(kWriteThreads), smem, st,
+                  r, a);
+}
+
+cudaError_t launch_qcache_queries(const RopeArgs& r, const QAttnArgs& a, cudaStream_t st) {
+  return launch_k(qcache_query_kernel, dim3(a.n, a.B), dim3(256), 0, st, r, a);
+}
+
+int qcache_splits(int max_pages, int n, int window, int split) {
+  const int64_t all = (static_cast<int64_t>(max_pages) * kPg + split - 1) / split;
+  if (window == 0) return static_cast<int>(all);
+  // keys of the rows span at most window + n - 1 positions
+  const int64_t some = (static_cast<int64_t>(window) + n - 2) / split + 2;
+  return static_cast<int>(some < all ? some : all);
+}
+
+cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
+  return launch_k(qcache_attn_plain_kernel, dim3(a.rows, a.c.n_kv_heads, a.B), dim3(128), 0, st, a);
+}
+
+}  // namespace sv

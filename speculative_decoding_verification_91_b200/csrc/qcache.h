@@ -1,0 +1,111 @@
+// Rotary positions and the 8-bit paged cache: arguments of the kernels and
+// their launchers, shared by the C ABI (api_qcache.cu) and the kernel files.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace sv {
+
+constexpr int kMaxPairs = SPEC_ROPE_MAX_DIM / 2;
+
+// A rotary configuration as the kernels take it: turns[j] = f_j / (2 pi), so
+// the angle's reduction is exact (a subtraction of a whole number).
+struct RopeArgs {
+  int layout, span, n_rot;
+  double magnitude;
+  double turns[kMaxPairs];
+};
+
+// (c, s) of pair j at a position, in binary64.  The product of a position
+// below 2^31 and a frequency is off by at most 2^-53 of itself.
+__device__ __forceinline__ void rope_turn(int pos, double turns, double& c, double& s) {
+  const double t = static_cast<double>(pos) * turns;
+  sincospi(2.0 * (t - rint(t)), &s, &c);
+}
+
+// ---------------------------------------------------------------- spec_rope
+struct RopeOpArgs {
+  const void* x;
+  void* out;
+  int64_t x_row, x_head, out_row, out_head;   // strides in elements
+  const int32_t* positions;
+  int n_rows, n_heads, dim, inverse;
+};
+cudaError_t launch_rope(const RopeArgs& r, const RopeOpArgs& a, int dtype, cudaStream_t st);
+
+// ------------------------------------------------------------- 8-bit cache
+struct QCacheArgs {
+  int dim, n_kv_heads, num_pages, max_pages, block;   // block: tokens per scale
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  unsigned* status;
+};
+
+struct QWriteArgs {
+  QCacheArgs c;
+  int B, n;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t k_row, v_row;
+};
+cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st);
+
+// Queries of the attention: row r = i * G + g of (sequence, KV head) is query
+// head h * G + g at position L + q_offset + i.
+struct QAttnArgs {
+  QCacheArgs c;
+  int B, n, G, rows;            // rows = n * G per (sequence, KV head)
+  int q_offset, kv_extra, window, split, n_splits;
+  const uint16_t* q;
+  int64_t q_row;
+  float scale_log2;             // softmax scale * log2(e)
+  uint8_t* q_codes;             // [2][B * Hkv * rows][dim]: q = (code0 + code1) * q_scale
+  float* q_scale;               // [B * Hkv * rows]
+  float* part_o;                // [B * Hkv][n_splits][rows][dim]
+  float2* part_ml;              // [B * Hkv][n_splits][rows] (reference, sum of exponentials)
+  uint16_t* out;
+};
+cudaError_t launch_qcache_queries(const RopeArgs& r, const QAttnArgs& a, cudaStream_t st);
+cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st);
+
+// Absolute splits that rows of a sequence can touch.
+int qcache_splits(int max_pages, int n, int window, int split);
+
+// ---------------------------------------------------------------- e4m3
+// Two binary32 values to e4m3 codes (nearest, ties to even; beyond 448: 448;
+// NaN: the NaN code); lo in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+// Two codes to their values (exact).
+__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(codes)));
+  float2 f;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h2));
+  return f;
+}
+// Least e in [-100, 100] with amax <= 448 * 2^e (448 = 1.75 * 2^8): amax =
+// 1.m * 2^x needs e = x - 8, one more when 1.m > 1.75.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, -100), 100);
+}
+__device__ __forceinline__ float pow2f(int e) {   // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+}  // namespace sv
