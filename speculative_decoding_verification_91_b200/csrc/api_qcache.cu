@@ -106,7 +106,7 @@ bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_page
   s->n_splits = qcache_splits(max_pages, n, window, split_of(c));
   if (s->n_splits > kMaxQSplits) return false;
   const uint64_t rows = (uint64_t)B * n * n_q_heads;     // (sequence, KV head, row)
-  if (rows > 0x7fffffffull) return false;
+  if (rows > 0x3fffffffull) return false;                // row indices of both codes
   const uint64_t slots = rows * s->n_splits, D = c->head_dim;
   size_t off = kWsHeaderBytes;
   s->codes = off;   off = up256(off + 2 * rows * D);

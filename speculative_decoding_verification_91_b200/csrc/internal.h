@@ -14,6 +14,10 @@ namespace sv {
 // fails (the caller reports SPEC_ECUDA) or the layout is not encodable.
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows, uint32_t box_cols, uint64_t row_stride = 0);
+// 2D row-major tensor of bytes [rows][cols], box {box_cols, box_rows} with
+// box_cols = 128, 128-byte swizzle, zero fill outside the tensor.
+bool make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                     uint32_t box_rows, uint32_t box_cols);
 // 3D row-major bf16 tensor [d2][d1][d0] (strides in elements), box {b0, b1, b2},
 // 128-byte swizzle (b0 * 2 must be 128), zero fill outside the tensor.
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,

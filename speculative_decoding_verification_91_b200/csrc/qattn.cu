@@ -1,0 +1,798 @@
+// Split-KV attention over the 8-bit paged cache on the 5th-generation tensor
+// cores (sm_100a), persistent, e4m3 in both products.
+//
+//   s_ij = q_scale_i k_scale_j scale (q_i . k_j)      p_ij = 2^(s_ij log2 e - m_i)
+//   out_i = sum_j p_ij v_scale_j v_j / sum_j p_ij
+//
+// The cache is e4m3, so the products run in kind::f8f6f4 on the pages as TMA
+// brought them, with no conversion of K or V.  The bf16 side of each product is
+// held in two e4m3 codes whose sum keeps 8 bits: queries q = c0 + c1 (written
+// by the query kernel; two MMA passes into one accumulator) and weights p = w0 +
+// w1 / 16 (w1 the rounding error of w0, stacked under w0 in the M dimension, so
+// one pass gives both sums, in lanes r and 64 + r of the accumulator).
+//
+// Work item = (sequence, KV head, block of RP query rows, absolute split of
+// split_tokens keys); items are ordered and every CTA (one per SM) takes those
+// that start in an equal share of all key blocks.  19 warps:
+//   warp 0     TMA producer: keys, then values, of 128-key blocks (two pages)
+//              into a ring of kUnits units of 128 x dim bytes, and the queries.
+//   warp 1     allocates TMEM; one thread issues the MMAs: S[rows][128 keys] = Q
+//              K^T (A = Q, B = K, both K-major), two buffers; O[rows][dim] += P V
+//              (A = P, K-major, B = V as stored, MN-major).
+//   warp 2     page ids -> the item's scales in shared memory, an item ahead.
+//   warps 3-18 softmax: thread = (query row, 32 of the block's keys).  A row's
+//              reference m moves only when a block exceeds it by 2^kLazy (one
+//              barrier vote per block); the v scale is folded into m and p
+//              (p v_scale <= 2^kLazy), so blocks of any scale share one
+//              accumulator; the sum of p is kept in binary32.
+//
+// Value rows of keys outside the item's range or on pages that were not loaded
+// are zeroed in shared memory before P V, so stale slots (NaN codes among them)
+// never reach it.  Key blocks start at absolute multiples of 128 and a row's
+// weights depend on its own scores only, so a row's partial depends neither on n
+// nor on the batch, its row slot or the CTA.  Every wait is bounded.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "qcache.h"
+#include "tc_common.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int kBlk = 128;                  // keys per block
+constexpr int kPg = SPEC_PAGE_SIZE;
+constexpr int kSoftWarps = 16;
+constexpr int kFirstSoft = 3;
+constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
+constexpr uint32_t kSmemMax = 227u * 1024u;
+constexpr uint32_t kTail = 8192;
+constexpr uint32_t kPBytes = 128 * kBlk;   // w0 rows 0..63, w1 rows 64..127
+constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
+// p v_scale <= 2^kLazy; in code units times 2^kUnit: at most 362 < 448
+constexpr float kLazy = 1.5f;
+constexpr float kUnit = 128.f;
+constexpr float kLow = 16.f;               // w1 is stored times 16
+constexpr float kNoKey = -1e30f;           // reference of a row that has seen no key
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D (+)= A . B, e4m3 in, binary32 accumulation (K = 32 per instruction)
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: D binary32, A and B e4m3, M = 128, N = n,
+// A K-major, B K-major or MN-major.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int D, int RP>
+struct Cfg {
+  static constexpr uint32_t kUnit_ = kBlk * D;                  // one block's keys or values
+  static constexpr uint32_t kQBytes = 2u * RP * D;              // [code][atom][RP rows][128 B]
+  static constexpr uint32_t bytes(int units, int qb) {
+    return 1024u + qb * kQBytes + 2 * kPBytes + units * kUnit_ + kTail;
+  }
+  static constexpr int kQBufs = bytes(4, 2) <= kSmemMax ? 2 : 1;
+  static constexpr int kUnits = bytes(8, kQBufs) <= kSmemMax   ? 8
+                                : bytes(6, kQBufs) <= kSmemMax ? 6
+                                : bytes(5, kQBufs) <= kSmemMax ? 5
+                                                               : 4;
+  static constexpr uint32_t kOffP = kQBufs * kQBytes;
+  static constexpr uint32_t kOffRing = kOffP + 2 * kPBytes;
+  static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnit_;
+  static constexpr uint32_t kSmem = 1024 + kOffTail + kTail;
+  static_assert(kSmem <= kSmemMax, "shared memory");
+  // a query tile of RP rows is read as 128 rows (the lanes past RP are unused):
+  // what follows it has to be shared memory too
+  static_assert(2 * kPBytes + kUnits * kUnit_ >= 128u * 128u, "query tile overrun");
+};
+
+// Keys any row of a sequence may see, as whole blocks; none: blocks = 0.
+struct SeqKeys {
+  int lo, hi, splits, blocks;
+};
+__device__ __forceinline__ SeqKeys seq_keys(const QAttnArgs& a, int L) {
+  SeqKeys k{0, -1, 0, 0};
+  if (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * kPg) return k;
+  k.hi = min(L + a.kv_extra - 1, L + a.q_offset + a.n - 1);
+  k.lo = a.window > 0 ? max(0, L + a.q_offset - a.window + 1) : 0;
+  if (k.hi < k.lo) return k;
+  k.splits = k.hi / a.split - k.lo / a.split + 1;
+  k.blocks = k.hi / kBlk - k.lo / kBlk + 1;
+  return k;
+}
+
+// Walks the items of one CTA; every role keeps its own.
+struct Walker {
+  const QAttnArgs* a;
+  int RP, RB, per_b;       // rows and row blocks; (KV head, row block) pairs
+  int b, hr, sidx, L;
+  SeqKeys k;
+  long base, end, pos;     // key blocks before sequence b; where the CTA stops; this item's start
+  int lo, hi, blk0, nb;    // this item's keys and blocks (nb = 0: none)
+  bool fresh;              // the queries changed since the role last took them
+  __device__ bool valid() const { return b < a->B && pos < end; }
+  __device__ void settle() {   // (b, hr, sidx) may be one past its range
+    for (;;) {
+      if (b >= a->B) return;
+      if (sidx < k.splits && hr < per_b) break;
+      if (hr < per_b) {
+        sidx = 0;
+        ++hr;
+        fresh = true;
+      }
+      if (hr >= per_b) {
+        base += static_cast<long>(per_b) * k.blocks;
+        hr = sidx = 0;
+        fresh = true;
+        if (++b < a->B) {
+          L = a->c.seq_lens[b];
+          k = seq_keys(*a, L);
+          if (k.blocks == 0) hr = per_b;
+        }
+      }
+    }
+    const int s0 = (k.lo / a->split + sidx) * a->split;
+    const int start = max(s0, k.lo);
+    pos = base + static_cast<long>(hr) * k.blocks + (start / kBlk - k.lo / kBlk);
+    const int r0 = (hr % RB) * RP, r1 = min(a->rows, r0 + RP) - 1;
+    const int p0 = L + a->q_offset + r0 / a->G, p1 = L + a->q_offset + r1 / a->G;
+    lo = a->window > 0 ? max(start, p0 - a->window + 1) : start;
+    hi = min(min(s0 + a->split - 1, k.hi), p1);
+    blk0 = lo / kBlk;
+    nb = hi >= lo ? hi / kBlk - blk0 + 1 : 0;
+  }
+  __device__ void start(const QAttnArgs* args, int rp, const int* at, long base0, long end0) {
+    a = args;
+    RP = rp;
+    RB = (a->rows + RP - 1) / RP;
+    per_b = a->c.n_kv_heads * RB;
+    b = at[0];
+    hr = at[1];
+    sidx = at[2];
+    base = base0;
+    end = end0;
+    pos = 0;
+    lo = blk0 = nb = 0;
+    hi = -1;
+    fresh = true;
+    if (b < a->B) {
+      L = a->c.seq_lens[b];
+      k = seq_keys(*a, L);
+    }
+    settle();
+  }
+  __device__ void next() {
+    ++sidx;
+    settle();
+  }
+};
+
+__device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* fail) {
+  if (*fail) return false;
+  if (mbar_wait(bar, parity, status)) return true;
+  *fail = 1;
+  return false;
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constant__ CUtensorMap tk,
+                                                            const __grid_constant__ CUtensorMap tv,
+                                                            const __grid_constant__ CUtensorMap tq,
+                                                            const __grid_constant__ QAttnArgs a) {
+  using C = Cfg<D, RP>;
+  constexpr int NU = C::kUnits, QB = C::kQBufs, ATOMS = D / 128;
+  constexpr uint32_t kAtom = kBlk * 128;
+  constexpr uint32_t kColS = 256;            // score buffers behind the output's columns
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;
+  uint8_t* pbuf = smem + C::kOffP;
+  uint8_t* ring = smem + C::kOffRing;
+  uint8_t* tail = smem + C::kOffTail;
+  uint64_t* u_full = reinterpret_cast<uint64_t*>(tail);   // [NU]
+  uint64_t* u_empty = u_full + NU;                         // [NU]
+  uint64_t* q_full = u_empty + NU;                         // [2]
+  uint64_t* q_empty = q_full + 2;                          // [2]
+  uint64_t* s_full = q_empty + 2;                          // [2] by block parity
+  uint64_t* p_full = s_full + 2;                           // [2]
+  uint64_t* pv_done = p_full + 2;                          // [2]
+  uint64_t* sc_full = pv_done + 2;                         // [2] by item parity
+  uint64_t* sc_empty = sc_full + 2;                        // [2]
+  uint64_t* o_free = sc_empty + 2;
+  uint64_t* mma_done = o_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* at = reinterpret_cast<int*>(tmem_slot + 2);         // first item: b, (head, row block), split
+  long* span = reinterpret_cast<long*>(tail + 512);        // key blocks before it, and where to stop
+  float* red = reinterpret_cast<float*>(tail + 1024);      // [2 row halves][4 key groups][32 rows]
+  float* alpha_s = red + 256;                              // [2][32]
+  float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [2 items][kMaxScales]
+  float* vs_s = ks_s + 2 * kMaxScales;                     // < 0: page not there
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_empty[i], kSoftWarps);
+    }
+    mbar_init(o_free, kSoftWarps);
+    mbar_init(mma_done, 1);
+    *fail = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    prefetch_tmap(&tq);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  pdl_trigger();
+  pdl_wait();
+
+  const int RB = (a.rows + RP - 1) / RP, per_b = a.c.n_kv_heads * RB;
+  if (warp == 2) {
+    // ---- this CTA's share [x0, x1) of all key blocks and its first item
+    long total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      long n = 0;
+      if (b0 + lane < a.B) {
+        const int L = a.c.seq_lens[b0 + lane];
+        n = seq_keys(a, L).blocks;
+        if (blockIdx.x == 0 &&
+            (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * kPg))
+          flag_status(a.c.status, SPEC_DEV_BAD_LENGTH);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+      total += n * per_b;
+    }
+    const long x0 = static_cast<long>(blockIdx.x) * total / gridDim.x;
+    const long x1 = static_cast<long>(blockIdx.x + 1) * total / gridDim.x;
+    long pre = 0;
+    int found = a.B;
+    long found_pre = 0;
+    for (int b0 = 0; b0 < a.B && found == a.B && x1 > x0; b0 += 32) {
+      long n = 0;
+      if (b0 + lane < a.B) n = static_cast<long>(seq_keys(a, a.c.seq_lens[b0 + lane]).blocks) * per_b;
+      long incl = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const long excl = pre + incl - n;
+      const unsigned bal = __ballot_sync(0xffffffffu, n > 0 && x0 >= excl && x0 < excl + n);
+      if (bal) {
+        const int src = __ffs(bal) - 1;
+        found = b0 + src;
+        found_pre = __shfl_sync(0xffffffffu, excl, src);
+      }
+      pre += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      at[0] = found;
+      at[1] = at[2] = 0;
+      span[0] = found_pre;
+      span[1] = x1;
+      if (found < a.B) {
+        const SeqKeys k = seq_keys(a, a.c.seq_lens[found]);
+        const long rem = x0 - found_pre;
+        at[1] = static_cast<int>(rem / k.blocks);
+        const int r = static_cast<int>(rem % k.blocks), first = k.lo / kBlk, bps = a.split / kBlk;
+        // the first split that starts at or after block r of the sequence
+        at[2] = r == 0 ? 0 : (r + first + bps - 1) / bps - k.lo / a.split;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walker w;
+  w.start(&a, RP, at, span[0], span[1]);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t pol = RB > 1 ? policy_evict_normal() : policy_evict_first();
+      const uint64_t pol_q = policy_evict_normal();
+      const int plane = a.B * a.c.n_kv_heads * a.rows;
+      int nu = 0, nq = 0;
+      bool ok = true;
+      for (; ok && w.valid(); w.next()) {
+        if (w.nb == 0) continue;
+        const int h = w.hr / RB, r0 = (w.hr % RB) * RP;
+        if (w.fresh) {
+          const int qb = nq % QB;
+          if (nq >= QB && !(ok = fwait(&q_empty[qb], ((nq / QB) - 1) & 1, a.c.status, fail))) break;
+          mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
+          const int y = (w.b * a.c.n_kv_heads + h) * a.rows + r0;
+          for (int c = 0; c < 2; ++c)
+            for (int t = 0; t < ATOMS; ++t)
+              tma_load_2d(qbuf + qb * C::kQBytes + (c * ATOMS + t) * (RP * 128), &tq, &q_full[qb], t * 128,
+                          c * plane + y, pol_q);
+          ++nq;
+          w.fresh = false;
+        }
+        const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
+        for (int j = 0; ok && j < w.nb; ++j) {
+          int id[2];
+          uint32_t bytes = 0;
+          for (int p = 0; p < 2; ++p) {
+            const int pg = (w.blk0 + j) * 2 + p;
+            id[p] = -1;
+            if (pg * kPg <= w.hi && pg * kPg + kPg - 1 >= w.lo) id[p] = bt[pg];
+            if (id[p] < 0 || id[p] >= a.c.num_pages) id[p] = -1;
+            else bytes += kPg * D;
+          }
+          for (int kv = 0; kv < 2; ++kv) {
+            const int s = nu % NU;
+            if (nu >= NU && !(ok = fwait(&u_empty[s], ((nu / NU) - 1) & 1, a.c.status, fail))) break;
+            mbar_arrive_expect_tx(&u_full[s], bytes);
+            for (int p = 0; p < 2; ++p) {
+              if (id[p] < 0) continue;
+              const int y = (id[p] * a.c.n_kv_heads + h) * kPg;
+#pragma unroll
+              for (int t = 0; t < ATOMS; ++t)
+                tma_load_2d(ring + s * C::kUnit_ + t * kAtom + p * (kPg * 128), kv ? &tv : &tk, &u_full[s], t * 128,
+                            y, pol);
+            }
+            ++nu;
+          }
+        }
+      }
+      // every issued copy must land before the CTA may exit
+      for (int i = (nu > NU ? nu - NU : 0); i < nu; ++i) mbar_wait(&u_full[i % NU], (i / NU) & 1, a.c.status);
+      for (int i = (nq > QB ? nq - QB : 0); i < nq; ++i) mbar_wait(&q_full[i % QB], (i / QB) & 1, a.c.status);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      const uint32_t id_qk = idesc_e4m3(kBlk, false), id_pv = idesc_e4m3(D, true);
+      Walker wp = w;
+      while (w.valid() && w.nb == 0) w.next();
+      while (wp.valid() && wp.nb == 0) wp.next();
+      int js = 0, jp = 0, ip = 0;         // block in item (scores, P V); items begun by P V
+      int nqk = 0, npv = 0, nq = 0;       // blocks issued; query groups begun
+      bool waiting_q = false;
+      uint64_t t_last = 0;
+      uint32_t polls = 0;
+      while (wp.valid()) {
+        bool progressed = false;
+        if (npv < nqk) {                  // P V first: it frees a unit
+          const int u = 2 * npv + 1;
+          bool ready = mbar_test_wait(&p_full[npv & 1], (npv >> 1) & 1) &&
+                       mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
+          if (jp == 0 && ip > 0) ready = ready && mbar_test_wait(o_free, (ip - 1) & 1);
+          if (ready) {
+            tc_fence_after();
+            const uint32_t v_addr = smem_u32(ring + (u % NU) * C::kUnit_);
+            const uint32_t p_addr = smem_u32(pbuf + (npv & 1) * kPBytes);
+#pragma unroll
+            for (int kk = 0; kk < kBlk / 32; ++kk)
+              umma_e4m3(tmem, sw128_desc(p_addr + kk * 32), sw128_desc_mn(v_addr + kk * 4096, kAtom), id_pv,
+                        (jp > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&pv_done[npv & 1]);
+            umma_commit(&u_empty[u % NU]);
+            ++npv;
+            if (++jp >= wp.nb) {
+              jp = 0;
+              ++ip;
+              do wp.next();
+              while (wp.valid() && wp.nb == 0);
+            }
+            progressed = true;
+          }
+        }
+        if (w.valid() && nqk <= npv + 1) {
+          if (js == 0 && w.fresh && !waiting_q) {
+            if (nq > 0) umma_commit(&q_empty[(nq - 1) % QB]);   // the last group's scores are issued
+            ++nq;
+            waiting_q = true;
+          }
+          const int u = 2 * nqk, qb = (nq - 1) % QB;
+          bool ready = !waiting_q || mbar_test_wait(&q_full[qb], ((nq - 1) / QB) & 1);
+          ready = ready && mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
+          if (ready) {
+            waiting_q = false;
+            w.fresh = false;
+            tc_fence_after();
+            const uint32_t k_addr = smem_u32(ring + (u % NU) * C::kUnit_);
+            const uint32_t q_addr = smem_u32(qbuf + qb * C::kQBytes);
+            const uint32_t t_s = tmem + kColS + (nqk & 1) * kBlk;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                umma_e4m3(t_s, sw128_desc(q_addr + (c * ATOMS + (kk >> 2)) * (RP * 128) + (kk & 3) * 32),
+                          sw128_desc(k_addr + (kk >> 2) * kAtom + (kk & 3) * 32), id_qk, (c > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&s_full[nqk & 1]);
+            umma_commit(&u_empty[u % NU]);
+            ++nqk;
+            if (++js >= w.nb) {
+              js = 0;
+              do w.next();
+              while (w.valid() && w.nb == 0);
+            }
+            progressed = true;
+          }
+        }
+        if (progressed) {
+          polls = 0;
+        } else if ((++polls & 255u) != 0) {
+          __nanosleep(20);
+        } else {
+          const uint64_t now = globaltimer_ns();
+          if (polls == 256) t_last = now;
+          else if (now - t_last > kWaitNs || *fail) {
+            flag_status(a.c.status, SPEC_DEV_TIMEOUT);
+            *fail = 1;
+            break;
+          }
+        }
+      }
+      // nothing may be in flight when TMEM is freed
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0, a.c.status);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- scales
+    const int per_page = kPg / a.c.block;
+    int i = 0;
+    for (; w.valid(); w.next()) {
+      if (w.nb == 0) continue;
+      const int h = w.hr / RB;
+      if (i >= 2) fwait(&sc_empty[i & 1], ((i >> 1) - 1) & 1, a.c.status, fail);
+      const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
+      const int count = w.nb * (kBlk / a.c.block);
+      for (int e = lane; e < count; e += 32) {
+        const int key = w.blk0 * kBlk + e * a.c.block, pg = key / kPg;
+        float ks = 0.f, vs = -1.f;
+        if (pg * kPg <= w.hi && pg * kPg + kPg - 1 >= w.lo) {
+          const int id = bt[pg];
+          if (id >= 0 && id < a.c.num_pages) {
+            const int64_t sc = (static_cast<int64_t>(id) * a.c.n_kv_heads + h) * per_page + (key % kPg) / a.c.block;
+            ks = a.c.ks[sc];
+            vs = a.c.vs[sc];
+          } else {
+            flag_status(a.c.status, SPEC_DEV_BAD_PAGE);
+          }
+        }
+        ks_s[(i & 1) * kMaxScales + e] = ks;
+        vs_s[(i & 1) * kMaxScales + e] = vs;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc_full[i & 1]);
+      ++i;
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int quad = warp & 3, cg = (warp - kFirstSoft) >> 2;     // TMEM lane quadrant, keys 32 cg ..
+    const int rh = quad & 1;                                      // row half: rows 32 rh + lane
+    const bool computes = quad < 2;                               // lanes of w0; the others hold w1's sums
+    const int row = rh * 32 + lane;
+    const int st = (warp - kFirstSoft) * 32 + lane;               // 0..511
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int bar_rows = 1 + rh, bar_cg = 3 + rh * 4 + cg;
+    const int bt_ = a.c.block;
+    float* red_r = red + rh * 128;
+    int g = 0, item = 0;
+    for (; w.valid(); w.next()) {
+      const int h = w.hr / RB, r0 = (w.hr % RB) * RP;
+      const int nrows = min(a.rows - r0, RP);
+      const long slot = (static_cast<long>(w.b * a.c.n_kv_heads + h) * a.n_splits + w.sidx) * a.rows + r0;
+      if (w.nb == 0) {
+        if (cg == 0 && computes && row < nrows) __stcg(&a.part_ml[slot + row], make_float2(kNoKey, 0.f));
+        continue;
+      }
+      const bool half_used = rh * 32 < nrows;         // this pair of quadrants holds rows
+      const bool mine = computes && row < nrows;
+      const int p = w.L + a.q_offset + (r0 + row) / a.G;
+      const int row_lo = max(w.lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(w.hi, p);
+      float qs = mine ? a.q_scale[(static_cast<long>(w.b) * a.c.n_kv_heads + h) * a.rows + r0 + row] : 0.f;
+      qs = qs == qs ? qs * a.scale_log2 : 0.f;        // a NaN row's result is set by the combine
+      const float* ks = ks_s + (item & 1) * kMaxScales;
+      const float* vs = vs_s + (item & 1) * kMaxScales;
+      fwait(&sc_full[item & 1], (item >> 1) & 1, a.c.status, fail);
+      float mref = kNoKey, l = 0.f;
+      for (int j = 0; j < w.nb; ++j, ++g) {
+        const int kb = (w.blk0 + j) * kBlk, key0 = kb + cg * 32;
+        fwait(&s_full[g & 1], (g >> 1) & 1, a.c.status, fail);
+        tc_fence_after();
+        float s[32], f[2], vsc[2];
+        bool need = false;
+        float cand = -INFINITY;
+        if (half_used) {
+          if (mine) {
+            // warp-wide load below; scales of the 32 keys (two of 16-token blocks)
+            const int e0 = (j * kBlk + cg * 32) / bt_, e1 = (j * kBlk + cg * 32 + 16) / bt_;
+            vsc[0] = vs[e0];
+            vsc[1] = vs[e1];
+            f[0] = fminf(fmaxf(qs * ks[e0], 1e-30f), 3e38f);
+            f[1] = fminf(fmaxf(qs * ks[e1], 1e-30f), 3e38f);
+          }
+          __syncwarp();
+          if (computes) tmem_ld32(t_lane + kColS + (g & 1) * kBlk + cg * 32, s);
+          if (mine) {
+            if (key0 < row_lo || key0 + 31 > row_hi || vsc[0] < 0.f || vsc[1] < 0.f) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (key0 + c < row_lo || key0 + c > row_hi || vsc[c >> 4] < 0.f) s[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float mx = s[16 * u];
+#pragma unroll
+              for (int c = 1; c < 16; ++c) mx = fmaxf(mx, s[16 * u + c]);
+              // log2 of the scale, rounded up to a whole number, within the range the sums can take
+              const uint32_t ub = __float_as_uint(vsc[u]);
+              int lv = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7fffffu) ? 1 : 0);
+              lv = vsc[u] < 0.f ? 0 : max(-100, min(100, lv));
+              cand = fmaxf(cand, fmaf(mx, f[u], static_cast<float>(lv)));
+            }
+            need = cand > mref + kLazy;
+          }
+          __syncwarp();
+          if (bar_red_or(bar_rows, 256, need)) {
+            if (computes) red_r[cg * 32 + lane] = mine ? cand : -INFINITY;
+            named_bar(bar_rows, 256);
+            if (computes) {
+              const float bm = fmaxf(fmaxf(red_r[lane], red_r[32 + lane]), fmaxf(red_r[64 + lane], red_r[96 + lane]));
+              float al = 1.f;
+              if (bm > mref + kLazy) {
+                al = ex2(mref - bm);          // 0 while the row had no key
+                mref = bm;
+                l *= al;
+              }
+              if (cg == 0) alpha_s[rh * 32 + lane] = al;
+            }
+            named_bar(bar_rows, 256);
+            const float al = alpha_s[rh * 32 + lane];
+            if (j > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+              // the running sums of the moved rows (all earlier P V done)
+              fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 4; c += 8) {
+                uint32_t r8[8];
+                tmem_ld8_nowait(t_lane + cg * (D / 4) + c, r8);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r8[e] = __float_as_uint(__uint_as_float(r8[e]) * al);
+                tmem_st8(t_lane + cg * (D / 4) + c, r8);
+              }
+              tmem_st_wait();
+            }
+          }
+        }
+        // the P buffer was last read by P V of block g - 2
+        if (g >= 2) fwait(&pv_done[g & 1], ((g >> 1) - 1) & 1, a.c.status, fail);
+        if (mine) {
+          uint32_t w0[8], w1[8];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
+            const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
+            l += p0;
+            l += p1;
+            const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
+            uint16_t c0, c1;
+            uint32_t back;
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c0));
+            const __half2 rest = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLow));
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+            if ((c & 2) == 0) {
+              w0[c >> 2] = c0;
+              w1[c >> 2] = c1;
+            } else {
+              w0[c >> 2] |= static_cast<uint32_t>(c0) << 16;
+              w1[c >> 2] |= static_cast<uint32_t>(c1) << 16;
+            }
+          }
+          uint8_t* pp = pbuf + (g & 1) * kPBytes;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            *reinterpret_cast<uint4*>(pp + swz128(row, 2 * cg + u)) =
+                make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
+            *reinterpret_cast<uint4*>(pp + swz128(64 + row, 2 * cg + u)) =
+                make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
+          }
+        }
+        // ---- value rows no row of the item may use: zero them (four threads per key)
+        {
+          const int key = kb + (st >> 2);
+          const float kv = vs[(j * kBlk + (st >> 2)) / bt_];
+          if (key < w.lo || key > w.hi || kv < 0.f) {
+            const int u = 2 * g + 1;
+            fwait(&u_full[u % NU], (u / NU) & 1, a.c.status, fail);
+            uint8_t* vrow = ring + (u % NU) * C::kUnit_ + (st >> 2) * 128;
+#pragma unroll
+            for (int t = 0; t < ATOMS; ++t)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<uint4*>(vrow + t * kAtom + ((st & 3) * 2 + c) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g & 1]);
+      }
+      // ---- the item's sums: (m, l), and o = o0 + o1 / 16 through shared memory
+      // (this row half's part of the P buffers, which no MMA reads now)
+      fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
+      __syncwarp();
+      tc_fence_after();
+      if (half_used) {
+        if (computes) red_r[cg * 32 + lane] = l;
+        named_bar(bar_rows, 256);
+        if (cg == 0 && mine && !*fail) {
+          const float sum = (red_r[lane] + red_r[32 + lane]) + (red_r[64 + lane] + red_r[96 + lane]);
+          __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
+        }
+        float* stage = reinterpret_cast<float*>(pbuf + (cg & 1) * kPBytes + (64 * (cg >> 1) + 32 * rh) * 128);
+#pragma unroll 1
+        for (int c0 = cg * (D / 4); c0 < (cg + 1) * (D / 4); c0 += 32) {
+          float o[32];
+          tmem_ld32(t_lane + c0, o);
+          if (!computes) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) stage[c * 32 + (lane ^ c)] = o[c] * (1.f / (kUnit * kLow));
+          }
+          named_bar(bar_cg, 64);
+          if (computes) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float* x = &stage[c * 32 + (lane ^ c)];
+              *x = fmaf(o[c], 1.f / kUnit, *x);
+            }
+          }
+          named_bar(bar_cg, 64);
+          const int n = min(nrows - rh * 32, 32);
+          if (!*fail)
+            for (int r = quad >> 1; r < n; r += 2)
+              __stcg(a.part_o + (slot + rh * 32 + r) * D + c0 + lane, stage[lane * 32 + (r ^ lane)]);
+          named_bar(bar_cg, 64);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_free);
+        mbar_arrive(&sc_empty[item & 1]);
+      }
+      ++item;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row.
+// Four parts by absolute split index mod 4, each in ascending order, then the
+// parts in order: splits without a key of the row add nothing at fixed places,
+// so the order does not depend on where the list of splits starts.  One warp per
+// part, a CTA per row.
+__global__ void __launch_bounds__(128) qattn_combine_kernel(const __grid_constant__ QAttnArgs a) {
+  __shared__ float o_s[4][256];
+  __shared__ float l_s[4], m_s[4];
+  pdl_trigger();
+  pdl_wait();
+  const int r = blockIdx.x % a.rows, bh = blockIdx.x / a.rows;
+  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.c.dim, i = r / a.G, hq = h * a.G + r % a.G;
+  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + i) * (a.c.n_kv_heads * a.G) + hq) * D;
+  const SeqKeys k = seq_keys(a, a.c.seq_lens[b]);
+  const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r;
+  float M = -INFINITY;
+  for (int s = threadIdx.x; s < k.splits; s += 128) M = fmaxf(M, __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows]).x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (lane == 0) m_s[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+  float o[8], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.f;
+  const int sf = k.splits ? k.lo / a.split : 0, per = D / 32;
+  for (int s = ((warp - sf) & 3); s < k.splits; s += 4) {
+    const float2 ml = __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows]);
+    if (ml.x <= kNoKey) continue;
+    const float wt = exp2f(ml.x - M);
+    const float* po = a.part_o + (slot0 + static_cast<int64_t>(s) * a.rows) * D + lane * per;
+    l = fmaf(wt, ml.y, l);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(po));
+    o[0] = fmaf(wt, x.x, o[0]);
+    o[1] = fmaf(wt, x.y, o[1]);
+    o[2] = fmaf(wt, x.z, o[2]);
+    o[3] = fmaf(wt, x.w, o[3]);
+    if (per == 8) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(po + 4));
+      o[4] = fmaf(wt, y.x, o[4]);
+      o[5] = fmaf(wt, y.y, o[5]);
+      o[6] = fmaf(wt, y.z, o[6]);
+      o[7] = fmaf(wt, y.w, o[7]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < per) o_s[warp][lane * per + e] = o[e];
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  const float den = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+  const float qs = a.q_scale[static_cast<int64_t>(bh) * a.rows + r];
+  for (int d = threadIdx.x; d < D; d += 128) {
+    const float x = ((o_s[0][d] + o_s[1][d]) + o_s[2][d]) + o_s[3][d];
+    dst[d] = den == 0.f ? 0 : f32_to_bf16(qs == qs ? x / den : qs);   // no key: zero
+  }
+}
+
+template <int D, int RP>
+cudaError_t launch_one(int grid, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                       const QAttnArgs& a, cudaStream_t st) {
+  auto kern = qattn_kernel<D, RP>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, RP>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D, RP>::kSmem, st, tk, tv, tq, a);
+}
+
+template <int D>
+cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                       const QAttnArgs& a, cudaStream_t st) {
+  if (rp == 16) return launch_one<D, 16>(grid, tk, tv, tq, a, st);
+  if (rp == 32) return launch_one<D, 32>(grid, tk, tv, tq, a, st);
+  return launch_one<D, 64>(grid, tk, tv, tq, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
+  const int D = a.c.dim, rp = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : 64;
+  const uint64_t rows = static_cast<uint64_t>(a.c.num_pages) * a.c.n_kv_heads * kPg;
+  const uint64_t qrows = 2ull * a.B * a.c.n_kv_heads * a.rows;
+  CUtensorMap tk, tv, tq;
+  if (!make_tmap_u8_2d(&tk, a.c.k, rows, D, kPg, 128) || !make_tmap_u8_2d(&tv, a.c.v, rows, D, kPg, 128) ||
+      !make_tmap_u8_2d(&tq, a.q_codes, qrows, D, rp, 128))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rp - 1) / rp) * a.n_splits;
+  const int grid = static_cast<int>(items < sms ? items : sms);
+  e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, tq, a, st) : launch_dim<128>(rp, grid, tk, tv, tq, a, st);
+  if (e != cudaSuccess) return e;
+  return launch_k(qattn_combine_kernel, dim3(a.B * a.c.n_kv_heads * a.rows), dim3(128), 0, st, a);
+}
+
+}  // namespace sv

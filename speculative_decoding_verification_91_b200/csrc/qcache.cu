@@ -1,5 +1,5 @@
-// The 8-bit paged cache: the append that quantises (spec_qcache_write), the
-// queries' form for the attention over it, and a plain attention kernel.
+// The 8-bit paged cache: the append that quantises (spec_qcache_write) and the
+// queries' form for the attention over it (qattn.cu).
 #include <math.h>
 
 #include "common.cuh"
@@ -182,74 +182,6 @@ __global__ void __launch_bounds__(256) qcache_query_kernel(const __grid_constant
   }
 }
 
-// A CTA per (row, KV head, sequence): four warps take the row's keys in turn,
-// each with its own running maximum and sums, joined at the end.
-__global__ void __launch_bounds__(128) qcache_attn_plain_kernel(const __grid_constant__ QAttnArgs a) {
-  __shared__ float o_s[4][256];
-  __shared__ float m_s[4], l_s[4];
-  pdl_trigger();
-  pdl_wait();
-  const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const QCacheArgs& c = a.c;
-  const int D = c.dim, per = D / 32, H = c.n_kv_heads;
-  const int i = r / a.G, g = r % a.G;
-  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + i) * H * a.G + h * a.G + g) * D;
-  const int L = c.seq_lens[b];
-  const bool fits = L >= 0 && static_cast<int64_t>(L) + a.kv_extra <= static_cast<int64_t>(c.max_pages) * kPg;
-  if (!fits && threadIdx.x == 0 && r == 0 && h == 0) flag_status(c.status, SPEC_DEV_BAD_LENGTH);
-  const int pos = L + a.q_offset + i;
-  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int hi = fits ? min(pos, L + a.kv_extra - 1) : -1;
-  const int64_t row = (static_cast<int64_t>(b) * H + h) * a.rows + r;
-  const int64_t plane = static_cast<int64_t>(a.B) * H * a.rows * D;
-  float q[8], o[8], m = -INFINITY, l = 0.f;
-  const float qsc = a.q_scale[row];
-  const float qs = qsc == qsc ? qsc * a.scale_log2 : 0.f;
-  for (int e = 0; e < 8; ++e) o[e] = q[e] = 0.f;
-  for (int e = 0; e < per; e += 2) {
-    const int64_t at = row * D + lane * per + e;
-    const float2 x = e4m3_values(*reinterpret_cast<const uint16_t*>(a.q_codes + at));
-    const float2 y = e4m3_values(*reinterpret_cast<const uint16_t*>(a.q_codes + plane + at));
-    q[e] = x.x + y.x;
-    q[e + 1] = x.y + y.y;
-  }
-  for (int j = lo + warp; j <= hi; j += 4) {
-    const int page = c.block_table[static_cast<int64_t>(b) * c.max_pages + j / kPg];
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
-      continue;
-    }
-    const int64_t head = static_cast<int64_t>(page) * H + h;
-    const int64_t at = (head * kPg + j % kPg) * D + lane * per;
-    const int64_t sc = head * (kPg / c.block) + (j % kPg) / c.block;
-    float s = 0.f, v[8];
-    for (int e = 0; e < per; e += 2) {
-      const float2 kk = e4m3_values(*reinterpret_cast<const uint16_t*>(c.k + at + e));
-      const float2 vv = e4m3_values(*reinterpret_cast<const uint16_t*>(c.v + at + e));
-      s += q[e] * kk.x + q[e + 1] * kk.y;
-      v[e] = vv.x;
-      v[e + 1] = vv.y;
-    }
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= qs * c.ks[sc];
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn), pv = p * c.vs[sc];
-    for (int e = 0; e < per; ++e) o[e] = o[e] * al + pv * v[e];
-    l = l * al + p;
-    m = mn;
-  }
-  for (int e = 0; e < per; ++e) o_s[warp][lane * per + e] = o[e];
-  if (lane == 0) m_s[warp] = m, l_s[warp] = l;
-  __syncthreads();
-  const float M = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
-  float den = 0.f;
-  for (int w = 0; w < 4; ++w) den += m_s[w] == -INFINITY ? 0.f : l_s[w] * exp2f(m_s[w] - M);
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float x = 0.f;
-    for (int w = 0; w < 4; ++w) x += m_s[w] == -INFINITY ? 0.f : o_s[w][d] * exp2f(m_s[w] - M);
-    dst[d] = den == 0.f ? 0 : f32_to_bf16(qsc == qsc ? x / den : qsc);
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st) {
@@ -272,10 +204,6 @@ int qcache_splits(int max_pages, int n, int window, int split) {
   // keys of the rows span at most window + n - 1 positions
   const int64_t some = (static_cast<int64_t>(window) + n - 2) / split + 2;
   return static_cast<int>(some < all ? some : all);
-}
-
-cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
-  return launch_k(qcache_attn_plain_kernel, dim3(a.rows, a.c.n_kv_heads, a.B), dim3(128), 0, st, a);
 }
 
 }  // namespace sv
