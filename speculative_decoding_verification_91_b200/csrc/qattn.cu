@@ -13,14 +13,19 @@
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
-// that start in an equal share of all key blocks.  19 warps:
+// that start in an equal share of all key blocks.  11 warps:
 //   warp 0     TMA producer: keys, then values, of 128-key blocks (two pages)
-//              into a ring of kUnits units of 128 x dim bytes, and the queries.
-//   warp 1     allocates TMEM; one thread issues the MMAs: S[rows][128 keys] = Q
+//              into a ring of kUnits units of 128 x dim bytes, and the queries,
+//              128 / RP copies of them one below the other in the tile.
+//   warp 1     allocates TMEM; one thread issues the MMAs: S[128][128 keys] = Q
 //              K^T (A = Q, B = K, both K-major), two buffers; O[rows][dim] += P V
 //              (A = P, K-major, B = V as stored, MN-major).
 //   warp 2     page ids -> the item's scales in shared memory, an item ahead.
-//   warps 3-18 softmax: thread = (query row, 32 of the block's keys).  A row's
+//   warps 3-10 softmax: a thread takes one query row and 128 / (256 / RP) of the
+//              block's keys.  The copies of the queries give every TMEM lane
+//              quadrant, and so every scheduler, an equal part of the keys
+//              (one copy in lanes 0..RP-1 left all of the work to one or two
+//              schedulers: 4300 clocks a block instead of TUNED).  A row's
 //              reference m moves only when a block exceeds it by 2^kLazy (one
 //              barrier vote per block); the v scale is folded into m and p
 //              (p v_scale <= 2^kLazy), so blocks of any scale share one
@@ -44,17 +49,20 @@ namespace sv {
 namespace {
 
 constexpr int kBlk = 128;                  // keys per block
+constexpr int kLgBlk = 7;
 constexpr int kPg = SPEC_PAGE_SIZE;
-constexpr int kSoftWarps = 16;
+constexpr int kSoftWarps = 8;
 constexpr int kFirstSoft = 3;
 constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
 constexpr uint32_t kSmemMax = 227u * 1024u;
 constexpr uint32_t kTail = 8192;
 constexpr uint32_t kPBytes = 128 * kBlk;   // w0 rows 0..63, w1 rows 64..127
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
-// p v_scale <= 2^kLazy; in code units times 2^kUnit: at most 362 < 448
-constexpr float kLazy = 1.5f;
-constexpr float kUnit = 128.f;
+// p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448.  A larger
+// kLazy moves the reference less often, a larger kUnit keeps smaller weights
+// (w1's least step is 2^-9 / (kUnit kLow) = 2^-18 of the reference).
+constexpr float kLazy = 3.5f;
+constexpr float kUnit = 32.f;
 constexpr float kLow = 16.f;               // w1 is stored times 16
 constexpr float kNoKey = -1e30f;           // reference of a row that has seen no key
 
@@ -80,26 +88,19 @@ __device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn) {
   return (1u << 4) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int D, int RP>
+template <int D>
 struct Cfg {
-  static constexpr uint32_t kUnit_ = kBlk * D;                  // one block's keys or values
-  static constexpr uint32_t kQBytes = 2u * RP * D;              // [code][atom][RP rows][128 B]
-  static constexpr uint32_t bytes(int units, int qb) {
-    return 1024u + qb * kQBytes + 2 * kPBytes + units * kUnit_ + kTail;
-  }
-  static constexpr int kQBufs = bytes(4, 2) <= kSmemMax ? 2 : 1;
-  static constexpr int kUnits = bytes(8, kQBufs) <= kSmemMax   ? 8
-                                : bytes(6, kQBufs) <= kSmemMax ? 6
-                                : bytes(5, kQBufs) <= kSmemMax ? 5
-                                                               : 4;
+  static constexpr uint32_t kUnitBytes = kBlk * D;              // one block's keys or values
+  static constexpr uint32_t kQBytes = 2u * 128u * D;            // [code][atom][128 rows][128 B]
+  // two P and query buffers where they leave room for the ring (dim 128)
+  static constexpr int kPBufs = D == 128 ? 2 : 1;
+  static constexpr int kQBufs = D == 128 ? 2 : 1;
+  static constexpr int kUnits = D == 128 ? 7 : 4;
   static constexpr uint32_t kOffP = kQBufs * kQBytes;
-  static constexpr uint32_t kOffRing = kOffP + 2 * kPBytes;
-  static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnit_;
+  static constexpr uint32_t kOffRing = kOffP + kPBufs * kPBytes;
+  static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnitBytes;
   static constexpr uint32_t kSmem = 1024 + kOffTail + kTail;
   static_assert(kSmem <= kSmemMax, "shared memory");
-  // a query tile of RP rows is read as 128 rows (the lanes past RP are unused):
-  // what follows it has to be shared memory too
-  static_assert(2 * kPBytes + kUnits * kUnit_ >= 128u * 128u, "query tile overrun");
 };
 
 // Keys any row of a sequence may see, as whole blocks; none: blocks = 0.
@@ -120,66 +121,68 @@ __device__ __forceinline__ SeqKeys seq_keys(const QAttnArgs& a, int L) {
 // Walks the items of one CTA; every role keeps its own.
 struct Walker {
   const QAttnArgs* a;
-  int RP, RB, per_b;       // rows and row blocks; (KV head, row block) pairs
-  int b, hr, sidx, L;
+  int RP, RB;              // rows of a block, row blocks
+  int b, h, rb, sidx, L;
+  int split0, p0, p1;      // the sequence's first split; positions of the row block's first and last row
   SeqKeys k;
-  long base, end, pos;     // key blocks before sequence b; where the CTA stops; this item's start
+  long base, end, pos;     // key blocks before (b, h, rb); where the CTA stops; this item's start
   int lo, hi, blk0, nb;    // this item's keys and blocks (nb = 0: none)
   bool fresh;              // the queries changed since the role last took them
   __device__ bool valid() const { return b < a->B && pos < end; }
-  __device__ void settle() {   // (b, hr, sidx) may be one past its range
-    for (;;) {
-      if (b >= a->B) return;
-      if (sidx < k.splits && hr < per_b) break;
-      if (hr < per_b) {
-        sidx = 0;
-        ++hr;
-        fresh = true;
-      }
-      if (hr >= per_b) {
-        base += static_cast<long>(per_b) * k.blocks;
-        hr = sidx = 0;
-        fresh = true;
-        if (++b < a->B) {
-          L = a->c.seq_lens[b];
-          k = seq_keys(*a, L);
-          if (k.blocks == 0) hr = per_b;
-        }
-      }
-    }
-    const int s0 = (k.lo / a->split + sidx) * a->split;
-    const int start = max(s0, k.lo);
-    pos = base + static_cast<long>(hr) * k.blocks + (start / kBlk - k.lo / kBlk);
-    const int r0 = (hr % RB) * RP, r1 = min(a->rows, r0 + RP) - 1;
-    const int p0 = L + a->q_offset + r0 / a->G, p1 = L + a->q_offset + r1 / a->G;
+  __device__ void load_seq() {
+    L = a->c.seq_lens[b];
+    k = seq_keys(*a, L);
+    split0 = k.lo / a->split;
+  }
+  __device__ void load_rows() {
+    const int r0 = rb * RP, r1 = min(a->rows, r0 + RP) - 1;
+    p0 = L + a->q_offset + r0 / a->G;
+    p1 = L + a->q_offset + r1 / a->G;
+    fresh = true;
+  }
+  __device__ void derive() {
+    const int s0 = (split0 + sidx) * a->split, start = max(s0, k.lo);
+    pos = base + ((start >> kLgBlk) - (k.lo >> kLgBlk));
     lo = a->window > 0 ? max(start, p0 - a->window + 1) : start;
     hi = min(min(s0 + a->split - 1, k.hi), p1);
-    blk0 = lo / kBlk;
-    nb = hi >= lo ? hi / kBlk - blk0 + 1 : 0;
+    blk0 = lo >> kLgBlk;
+    nb = hi >= lo ? (hi >> kLgBlk) - blk0 + 1 : 0;
+  }
+  __device__ void next_rows() {   // the next (b, h, rb) that has keys, its first split
+    sidx = 0;
+    base += k.blocks;
+    if (++rb == RB) {
+      rb = 0;
+      if (++h == a->c.n_kv_heads) {
+        h = 0;
+        do {
+          if (++b >= a->B) return;
+          load_seq();
+        } while (k.blocks == 0);
+      }
+    }
+    load_rows();
+    derive();
+  }
+  __device__ void next() {
+    if (++sidx < k.splits) derive();
+    else next_rows();
   }
   __device__ void start(const QAttnArgs* args, int rp, const int* at, long base0, long end0) {
     a = args;
     RP = rp;
     RB = (a->rows + RP - 1) / RP;
-    per_b = a->c.n_kv_heads * RB;
     b = at[0];
-    hr = at[1];
-    sidx = at[2];
-    base = base0;
     end = end0;
-    pos = 0;
-    lo = blk0 = nb = 0;
-    hi = -1;
-    fresh = true;
-    if (b < a->B) {
-      L = a->c.seq_lens[b];
-      k = seq_keys(*a, L);
-    }
-    settle();
-  }
-  __device__ void next() {
-    ++sidx;
-    settle();
+    if (b >= a->B) return;
+    load_seq();
+    h = at[1] / RB;
+    rb = at[1] % RB;
+    sidx = at[2];
+    base = base0 + static_cast<long>(at[1]) * k.blocks;
+    load_rows();
+    if (sidx < k.splits) derive();
+    else next_rows();
   }
 };
 
@@ -195,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
                                                             const __grid_constant__ CUtensorMap tv,
                                                             const __grid_constant__ CUtensorMap tq,
                                                             const __grid_constant__ QAttnArgs a) {
-  using C = Cfg<D, RP>;
-  constexpr int NU = C::kUnits, QB = C::kQBufs, ATOMS = D / 128;
+  using C = Cfg<D>;
+  constexpr int NU = C::kUnits, QB = C::kQBufs, PB = C::kPBufs, ATOMS = D / 128;
   constexpr uint32_t kAtom = kBlk * 128;
   constexpr uint32_t kColS = 256;            // score buffers behind the output's columns
   extern __shared__ uint8_t smem_raw[];
@@ -220,8 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* at = reinterpret_cast<int*>(tmem_slot + 2);         // first item: b, (head, row block), split
   long* span = reinterpret_cast<long*>(tail + 512);        // key blocks before it, and where to stop
-  float* red = reinterpret_cast<float*>(tail + 1024);      // [2 row halves][4 key groups][32 rows]
-  float* alpha_s = red + 256;                              // [2][32]
+  float* red = reinterpret_cast<float*>(tail + 1024);      // [threads of a row][rows]
   float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [2 items][kMaxScales]
   float* vs_s = ks_s + 2 * kMaxScales;                     // < 0: page not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,19 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       bool ok = true;
       for (; ok && w.valid(); w.next()) {
         if (w.nb == 0) continue;
-        const int h = w.hr / RB, r0 = (w.hr % RB) * RP;
-        if (w.fresh) {
-          const int qb = nq % QB;
-          if (nq >= QB && !(ok = fwait(&q_empty[qb], ((nq / QB) - 1) & 1, a.c.status, fail))) break;
-          mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
-          const int y = (w.b * a.c.n_kv_heads + h) * a.rows + r0;
-          for (int c = 0; c < 2; ++c)
-            for (int t = 0; t < ATOMS; ++t)
-              tma_load_2d(qbuf + qb * C::kQBytes + (c * ATOMS + t) * (RP * 128), &tq, &q_full[qb], t * 128,
-                          c * plane + y, pol_q);
-          ++nq;
-          w.fresh = false;
-        }
         const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
         for (int j = 0; ok && j < w.nb; ++j) {
           int id[2];
@@ -356,13 +345,28 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             mbar_arrive_expect_tx(&u_full[s], bytes);
             for (int p = 0; p < 2; ++p) {
               if (id[p] < 0) continue;
-              const int y = (id[p] * a.c.n_kv_heads + h) * kPg;
+              const int y = (id[p] * a.c.n_kv_heads + w.h) * kPg;
 #pragma unroll
               for (int t = 0; t < ATOMS; ++t)
-                tma_load_2d(ring + s * C::kUnit_ + t * kAtom + p * (kPg * 128), kv ? &tv : &tk, &u_full[s], t * 128,
-                            y, pol);
+                tma_load_2d(ring + s * C::kUnitBytes + t * kAtom + p * (kPg * 128), kv ? &tv : &tk, &u_full[s],
+                            t * 128, y, pol);
             }
             ++nu;
+          }
+          // new queries behind the item's first block: their buffer may still
+          // be in use, and that must not hold back the first copies
+          if (ok && w.fresh) {
+            const int qb = nq % QB;
+            if (nq >= QB && !(ok = fwait(&q_empty[qb], ((nq / QB) - 1) & 1, a.c.status, fail))) break;
+            mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
+            const int y = (w.b * a.c.n_kv_heads + w.h) * a.rows + w.rb * RP;
+            for (int c = 0; c < 2; ++c)
+              for (int t = 0; t < ATOMS; ++t)
+                for (int r = 0; r < 128; r += RP)
+                  tma_load_2d(qbuf + qb * C::kQBytes + (c * ATOMS + t) * (128 * 128) + r * 128, &tq, &q_full[qb],
+                              t * 128, c * plane + y, pol_q);
+            ++nq;
+            w.fresh = false;
           }
         }
       }
@@ -391,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           if (jp == 0 && ip > 0) ready = ready && mbar_test_wait(o_free, (ip - 1) & 1);
           if (ready) {
             tc_fence_after();
-            const uint32_t v_addr = smem_u32(ring + (u % NU) * C::kUnit_);
-            const uint32_t p_addr = smem_u32(pbuf + (npv & 1) * kPBytes);
+            const uint32_t v_addr = smem_u32(ring + (u % NU) * C::kUnitBytes);
+            const uint32_t p_addr = smem_u32(pbuf + (npv % PB) * kPBytes);
 #pragma unroll
             for (int kk = 0; kk < kBlk / 32; ++kk)
               umma_e4m3(tmem, sw128_desc(p_addr + kk * 32), sw128_desc_mn(v_addr + kk * 4096, kAtom), id_pv,
@@ -422,14 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             waiting_q = false;
             w.fresh = false;
             tc_fence_after();
-            const uint32_t k_addr = smem_u32(ring + (u % NU) * C::kUnit_);
+            const uint32_t k_addr = smem_u32(ring + (u % NU) * C::kUnitBytes);
             const uint32_t q_addr = smem_u32(qbuf + qb * C::kQBytes);
             const uint32_t t_s = tmem + kColS + (nqk & 1) * kBlk;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                umma_e4m3(t_s, sw128_desc(q_addr + (c * ATOMS + (kk >> 2)) * (RP * 128) + (kk & 3) * 32),
+                umma_e4m3(t_s, sw128_desc(q_addr + (c * ATOMS + (kk >> 2)) * (128 * 128) + (kk & 3) * 32),
                           sw128_desc(k_addr + (kk >> 2) * kAtom + (kk & 3) * 32), id_qk, (c > 0 || kk > 0) ? 1u : 0u);
             umma_commit(&s_full[nqk & 1]);
             umma_commit(&u_empty[u % NU]);
@@ -444,11 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         }
         if (progressed) {
           polls = 0;
-        } else if ((++polls & 255u) != 0) {
-          __nanosleep(20);
-        } else {
+        } else if ((++polls & 1023u) == 0) {
           const uint64_t now = globaltimer_ns();
-          if (polls == 256) t_last = now;
+          if (polls == 1024) t_last = now;
           else if (now - t_last > kWaitNs || *fail) {
             flag_status(a.c.status, SPEC_DEV_TIMEOUT);
             *fail = 1;
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     int i = 0;
     for (; w.valid(); w.next()) {
       if (w.nb == 0) continue;
-      const int h = w.hr / RB;
+      const int h = w.h;
       if (i >= 2) fwait(&sc_empty[i & 1], ((i >> 1) - 1) & 1, a.c.status, fail);
       const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
       const int count = w.nb * (kBlk / a.c.block);
@@ -492,111 +494,116 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------- softmax
-    const int quad = warp & 3, cg = (warp - kFirstSoft) >> 2;     // TMEM lane quadrant, keys 32 cg ..
-    const int rh = quad & 1;                                      // row half: rows 32 rh + lane
-    const bool computes = quad < 2;                               // lanes of w0; the others hold w1's sums
+    constexpr int KW = RP / 2;                 // keys of a block a thread takes
+    constexpr int NG = kBlk / KW;              // threads of a row
+    const int quad = warp & 3, cg = (warp - kFirstSoft) >> 2;     // TMEM lane quadrant; first or second half of its keys
+    const int rh = RP == 64 ? quad & 1 : 0;                       // row half: rows 32 rh + lane
+    const int grp = (RP == 64 ? quad >> 1 : quad) * 2 + cg;       // keys KW grp .. of the block
     const int row = rh * 32 + lane;
-    const int st = (warp - kFirstSoft) * 32 + lane;               // 0..511
+    const int st = (warp - kFirstSoft) * 32 + lane;               // 0..255
+    const bool sums = RP == 64 || (quad & 1) == 0;                // lanes that hold sums of w0 (quadrants 0, 1) or w1
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int bar_rows = 1 + rh, bar_cg = 3 + rh * 4 + cg;
-    const int bt_ = a.c.block;
-    float* red_r = red + rh * 128;
+    const int bar_rows = 1 + rh, bar_cg = 3 + rh * 2 + cg;
+    constexpr int kRowThreads = RP == 64 ? 128 : 256;
+    const int lg_bt = 31 - __clz(a.c.block);
+    float* red_r = red + rh * (NG * 32);
     int g = 0, item = 0;
     for (; w.valid(); w.next()) {
-      const int h = w.hr / RB, r0 = (w.hr % RB) * RP;
-      const int nrows = min(a.rows - r0, RP);
-      const long slot = (static_cast<long>(w.b * a.c.n_kv_heads + h) * a.n_splits + w.sidx) * a.rows + r0;
+      const int r0 = w.rb * RP, nrows = min(a.rows - r0, RP);
+      const long bh = static_cast<long>(w.b) * a.c.n_kv_heads + w.h;
+      const long slot = (bh * a.n_splits + w.sidx) * a.rows + r0;
       if (w.nb == 0) {
-        if (cg == 0 && computes && row < nrows) __stcg(&a.part_ml[slot + row], make_float2(kNoKey, 0.f));
+        if (grp == 0 && row < nrows) __stcg(&a.part_ml[slot + row], make_float2(kNoKey, 0.f));
         continue;
       }
-      const bool half_used = rh * 32 < nrows;         // this pair of quadrants holds rows
-      const bool mine = computes && row < nrows;
+      const bool half_used = rh * 32 < nrows;         // these warps hold rows
+      const bool mine = row < nrows;
       const int p = w.L + a.q_offset + (r0 + row) / a.G;
       const int row_lo = max(w.lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(w.hi, p);
-      float qs = mine ? a.q_scale[(static_cast<long>(w.b) * a.c.n_kv_heads + h) * a.rows + r0 + row] : 0.f;
-      qs = qs == qs ? qs * a.scale_log2 : 0.f;        // a NaN row's result is set by the combine
+      float qs = mine ? a.q_scale[bh * a.rows + r0 + row] : 0.f;
+      qs = qs == qs ? qs * a.scale_log2 : 0.f;        // a NaN row's result is set at the end
       const float* ks = ks_s + (item & 1) * kMaxScales;
       const float* vs = vs_s + (item & 1) * kMaxScales;
       fwait(&sc_full[item & 1], (item >> 1) & 1, a.c.status, fail);
       float mref = kNoKey, l = 0.f;
       for (int j = 0; j < w.nb; ++j, ++g) {
-        const int kb = (w.blk0 + j) * kBlk, key0 = kb + cg * 32;
+        const int kb = (w.blk0 + j) << kLgBlk, key0 = kb + grp * KW;
+        constexpr int NE = KW / 16;                   // scales of the keys (one or two of 16-token blocks)
+        float s[KW], f[NE], vsc[NE];
+#pragma unroll
+        for (int u = 0; u < NE; ++u) {
+          const int e = ((j << kLgBlk) + grp * KW + 16 * u) >> lg_bt;
+          vsc[u] = vs[e];
+          f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), 3e38f);
+        }
         fwait(&s_full[g & 1], (g >> 1) & 1, a.c.status, fail);
+        __syncwarp();
         tc_fence_after();
-        float s[32], f[2], vsc[2];
-        bool need = false;
-        float cand = -INFINITY;
         if (half_used) {
-          if (mine) {
-            // warp-wide load below; scales of the 32 keys (two of 16-token blocks)
-            const int e0 = (j * kBlk + cg * 32) / bt_, e1 = (j * kBlk + cg * 32 + 16) / bt_;
-            vsc[0] = vs[e0];
-            vsc[1] = vs[e1];
-            f[0] = fminf(fmaxf(qs * ks[e0], 1e-30f), 3e38f);
-            f[1] = fminf(fmaxf(qs * ks[e1], 1e-30f), 3e38f);
+          const uint32_t t_s = t_lane + kColS + (g & 1) * kBlk + grp * KW;
+#pragma unroll
+          for (int c = 0; c < KW; c += 8) tmem_ld8_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[8]>(&s[c]));
+          tmem_ld_wait();
+          bool edge = key0 < row_lo || key0 + KW - 1 > row_hi;
+#pragma unroll
+          for (int u = 0; u < NE; ++u) edge |= vsc[u] < 0.f;
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < KW; ++c)
+              if (key0 + c < row_lo || key0 + c > row_hi || vsc[c >> 4] < 0.f) s[c] = -INFINITY;
+          }
+          float cand = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < NE; ++u) {
+            float m4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(fmaxf(s[16 * u + c], s[16 * u + 4 + c]), fmaxf(s[16 * u + 8 + c], s[16 * u + 12 + c]));
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            // log2 of the scale, rounded up to a whole number, within the range the sums can take
+            const uint32_t ub = __float_as_uint(vsc[u]);
+            int lv = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7fffffu) ? 1 : 0);
+            lv = vsc[u] < 0.f ? 0 : max(-100, min(100, lv));
+            cand = fmaxf(cand, fmaf(mx, f[u], static_cast<float>(lv)));
           }
           __syncwarp();
-          if (computes) tmem_ld32(t_lane + kColS + (g & 1) * kBlk + cg * 32, s);
-          if (mine) {
-            if (key0 < row_lo || key0 + 31 > row_hi || vsc[0] < 0.f || vsc[1] < 0.f) {
+          if (bar_red_or(bar_rows, kRowThreads, mine && cand > mref + kLazy)) {
+            red_r[grp * 32 + lane] = cand;
+            named_bar(bar_rows, kRowThreads);
+            float bm = red_r[lane];
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (key0 + c < row_lo || key0 + c > row_hi || vsc[c >> 4] < 0.f) s[c] = -INFINITY;
+            for (int e = 1; e < NG; ++e) bm = fmaxf(bm, red_r[e * 32 + lane]);
+            float al = 1.f;
+            if (mine && bm > mref + kLazy) {
+              al = ex2(mref - bm);            // 0 while the row had no key
+              mref = bm;
+              l *= al;
             }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float mx = s[16 * u];
-#pragma unroll
-              for (int c = 1; c < 16; ++c) mx = fmaxf(mx, s[16 * u + c]);
-              // log2 of the scale, rounded up to a whole number, within the range the sums can take
-              const uint32_t ub = __float_as_uint(vsc[u]);
-              int lv = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7fffffu) ? 1 : 0);
-              lv = vsc[u] < 0.f ? 0 : max(-100, min(100, lv));
-              cand = fmaxf(cand, fmaf(mx, f[u], static_cast<float>(lv)));
-            }
-            need = cand > mref + kLazy;
-          }
-          __syncwarp();
-          if (bar_red_or(bar_rows, 256, need)) {
-            if (computes) red_r[cg * 32 + lane] = mine ? cand : -INFINITY;
-            named_bar(bar_rows, 256);
-            if (computes) {
-              const float bm = fmaxf(fmaxf(red_r[lane], red_r[32 + lane]), fmaxf(red_r[64 + lane], red_r[96 + lane]));
-              float al = 1.f;
-              if (bm > mref + kLazy) {
-                al = ex2(mref - bm);          // 0 while the row had no key
-                mref = bm;
-                l *= al;
-              }
-              if (cg == 0) alpha_s[rh * 32 + lane] = al;
-            }
-            named_bar(bar_rows, 256);
-            const float al = alpha_s[rh * 32 + lane];
-            if (j > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+            if (j > 0 && sums && __any_sync(0xffffffffu, al != 1.f)) {
               // the running sums of the moved rows (all earlier P V done)
               fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
               __syncwarp();
               tc_fence_after();
+#pragma unroll 1
+              for (int c = cg * (D / 2); c < (cg + 1) * (D / 2); c += 32) {
+                uint32_t r8[4][8];
 #pragma unroll
-              for (int c = 0; c < D / 4; c += 8) {
-                uint32_t r8[8];
-                tmem_ld8_nowait(t_lane + cg * (D / 4) + c, r8);
+                for (int e = 0; e < 4; ++e) tmem_ld8_nowait(t_lane + c + 8 * e, r8[e]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) r8[e] = __float_as_uint(__uint_as_float(r8[e]) * al);
-                tmem_st8(t_lane + cg * (D / 4) + c, r8);
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) r8[e][x] = __float_as_uint(__uint_as_float(r8[e][x]) * al);
+                  tmem_st8(t_lane + c + 8 * e, r8[e]);
+                }
               }
               tmem_st_wait();
             }
           }
         }
-        // the P buffer was last read by P V of block g - 2
-        if (g >= 2) fwait(&pv_done[g & 1], ((g >> 1) - 1) & 1, a.c.status, fail);
-        if (mine) {
-          uint32_t w0[8], w1[8];
+        uint32_t w0[KW / 4], w1[KW / 4];
+        if (half_used) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
+          for (int c = 0; c < KW; c += 2) {
             const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
             const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
             l += p0;
@@ -616,28 +623,31 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
               w1[c >> 2] |= static_cast<uint32_t>(c1) << 16;
             }
           }
-          uint8_t* pp = pbuf + (g & 1) * kPBytes;
+        }
+        // the P buffer was last read by P V of block g - PB
+        if (g >= PB) fwait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1, a.c.status, fail);
+        if (mine) {
+          uint8_t* pp = pbuf + (g % PB) * kPBytes;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            *reinterpret_cast<uint4*>(pp + swz128(row, 2 * cg + u)) =
+          for (int u = 0; u < NE; ++u) {
+            *reinterpret_cast<uint4*>(pp + swz128(row, NE * grp + u)) =
                 make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
-            *reinterpret_cast<uint4*>(pp + swz128(64 + row, 2 * cg + u)) =
+            *reinterpret_cast<uint4*>(pp + swz128(64 + row, NE * grp + u)) =
                 make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
           }
         }
-        // ---- value rows no row of the item may use: zero them (four threads per key)
+        // ---- value rows no row of the item may use: zero them (two threads per key)
         {
-          const int key = kb + (st >> 2);
-          const float kv = vs[(j * kBlk + (st >> 2)) / bt_];
-          if (key < w.lo || key > w.hi || kv < 0.f) {
+          const int key = kb + (st >> 1);
+          if (key < w.lo || key > w.hi || vs[((j << kLgBlk) + (st >> 1)) >> lg_bt] < 0.f) {
             const int u = 2 * g + 1;
             fwait(&u_full[u % NU], (u / NU) & 1, a.c.status, fail);
-            uint8_t* vrow = ring + (u % NU) * C::kUnit_ + (st >> 2) * 128;
+            uint8_t* vrow = ring + (u % NU) * C::kUnitBytes + (st >> 1) * 128;
 #pragma unroll
             for (int t = 0; t < ATOMS; ++t)
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<uint4*>(vrow + t * kAtom + ((st & 3) * 2 + c) * 16) = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(vrow + t * kAtom + ((st & 1) * 4 + c) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
@@ -645,41 +655,45 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
-      // ---- the item's sums: (m, l), and o = o0 + o1 / 16 through shared memory
-      // (this row half's part of the P buffers, which no MMA reads now)
+      // ---- the item's (m, l) and o = (o0 + o1 / 16) / kUnit: the lanes of w1's
+      // sums pass theirs through shared memory (this row half's part of the P
+      // buffer, which no MMA reads now)
       fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
       __syncwarp();
       tc_fence_after();
       if (half_used) {
-        if (computes) red_r[cg * 32 + lane] = l;
-        named_bar(bar_rows, 256);
-        if (cg == 0 && mine && !*fail) {
-          const float sum = (red_r[lane] + red_r[32 + lane]) + (red_r[64 + lane] + red_r[96 + lane]);
-          __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
-        }
-        float* stage = reinterpret_cast<float*>(pbuf + (cg & 1) * kPBytes + (64 * (cg >> 1) + 32 * rh) * 128);
+        red_r[grp * 32 + lane] = l;           // every warp is past the last block's reductions
+        named_bar(bar_rows, kRowThreads);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < NG; e += 4)
+          sum += (red_r[e * 32 + lane] + red_r[e * 32 + 32 + lane]) + (red_r[e * 32 + 64 + lane] + red_r[e * 32 + 96 + lane]);
+        if (grp == 0 && mine && !*fail) __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
+        if (sums) {
+          float* stage = reinterpret_cast<float*>(pbuf + (64 * cg + 32 * rh) * 128);
+          float* po = a.part_o + (slot + row) * D;
 #pragma unroll 1
-        for (int c0 = cg * (D / 4); c0 < (cg + 1) * (D / 4); c0 += 32) {
-          float o[32];
-          tmem_ld32(t_lane + c0, o);
-          if (!computes) {
+          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 32) {
+            float o[32];
+            tmem_ld32(t_lane + c0, o);
+            if (quad >= 2) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) stage[c * 32 + (lane ^ c)] = o[c] * (1.f / (kUnit * kLow));
-          }
-          named_bar(bar_cg, 64);
-          if (computes) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float* x = &stage[c * 32 + (lane ^ c)];
-              *x = fmaf(o[c], 1.f / kUnit, *x);
+              for (int c = 0; c < 32; ++c) stage[c * 32 + lane] = o[c];
             }
+            named_bar(bar_cg, 64);
+            if (quad < 2 && mine && !*fail) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                float4 v;
+                v.x = fmaf(stage[c * 32 + lane], 1.f / kLow, o[c]) * (1.f / kUnit);
+                v.y = fmaf(stage[c * 32 + 32 + lane], 1.f / kLow, o[c + 1]) * (1.f / kUnit);
+                v.z = fmaf(stage[c * 32 + 64 + lane], 1.f / kLow, o[c + 2]) * (1.f / kUnit);
+                v.w = fmaf(stage[c * 32 + 96 + lane], 1.f / kLow, o[c + 3]) * (1.f / kUnit);
+                __stcg(reinterpret_cast<float4*>(po + c0 + c), v);
+              }
+            }
+            named_bar(bar_cg, 64);
           }
-          named_bar(bar_cg, 64);
-          const int n = min(nrows - rh * 32, 32);
-          if (!*fail)
-            for (int r = quad >> 1; r < n; r += 2)
-              __stcg(a.part_o + (slot + rh * 32 + r) * D + c0 + lane, stage[lane * 32 + (r ^ lane)]);
-          named_bar(bar_cg, 64);
         }
       }
       tc_fence_before();
@@ -761,15 +775,14 @@ cudaError_t launch_one(int grid, const CUtensorMap& tk, const CUtensorMap& tv, c
                        const QAttnArgs& a, cudaStream_t st) {
   auto kern = qattn_kernel<D, RP>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, RP>::kSmem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D, RP>::kSmem, st, tk, tv, tq, a);
+  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, tk, tv, tq, a);
 }
 
 template <int D>
 cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                        const QAttnArgs& a, cudaStream_t st) {
-  if (rp == 16) return launch_one<D, 16>(grid, tk, tv, tq, a, st);
   if (rp == 32) return launch_one<D, 32>(grid, tk, tv, tq, a, st);
   return launch_one<D, 64>(grid, tk, tv, tq, a, st);
 }
@@ -777,7 +790,7 @@ cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMa
 }  // namespace
 
 cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
-  const int D = a.c.dim, rp = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : 64;
+  const int D = a.c.dim, rp = a.rows <= 32 ? 32 : 64;
   const uint64_t rows = static_cast<uint64_t>(a.c.num_pages) * a.c.n_kv_heads * kPg;
   const uint64_t qrows = 2ull * a.B * a.c.n_kv_heads * a.rows;
   CUtensorMap tk, tv, tq;
