@@ -168,6 +168,9 @@ struct Walker {
     if (++sidx < k.splits) derive();
     else next_rows();
   }
+  __device__ void skip() {   // to the next item with keys
+    while (valid() && nb == 0) next();
+  }
   __device__ void start(const QAttnArgs* args, int rp, const int* at, long base0, long end0) {
     a = args;
     RP = rp;
@@ -185,6 +188,10 @@ struct Walker {
     else next_rows();
   }
 };
+
+// Ring units of block g's keys and values: K0 K1 V0 K2 V1 K3 V2 ..
+__device__ __forceinline__ int key_unit(int g) { return g == 0 ? 0 : 2 * g - 1; }
+__device__ __forceinline__ int value_unit(int g) { return 2 * g + 2; }
 
 __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* fail) {
   if (*fail) return false;
@@ -324,54 +331,82 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const uint64_t pol = RB > 1 ? policy_evict_normal() : policy_evict_first();
       const uint64_t pol_q = policy_evict_normal();
       const int plane = a.B * a.c.n_kv_heads * a.rows;
-      int nu = 0, nq = 0;
-      bool ok = true;
-      for (; ok && w.valid(); w.next()) {
-        if (w.nb == 0) continue;
-        const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
-        for (int j = 0; ok && j < w.nb; ++j) {
-          int id[2];
-          uint32_t bytes = 0;
-          for (int p = 0; p < 2; ++p) {
-            const int pg = (w.blk0 + j) * 2 + p;
-            id[p] = -1;
-            if (pg * kPg <= w.hi && pg * kPg + kPg - 1 >= w.lo) id[p] = bt[pg];
-            if (id[p] < 0 || id[p] >= a.c.num_pages) id[p] = -1;
-            else bytes += kPg * D;
-          }
-          for (int kv = 0; kv < 2; ++kv) {
-            const int s = nu % NU;
-            if (nu >= NU && !(ok = fwait(&u_empty[s], ((nu / NU) - 1) & 1, a.c.status, fail))) break;
-            mbar_arrive_expect_tx(&u_full[s], bytes);
-            for (int p = 0; p < 2; ++p) {
-              if (id[p] < 0) continue;
-              const int y = (id[p] * a.c.n_kv_heads + w.h) * kPg;
+      int last[NU];                       // unit last copied into each slot, -1: none
+      for (int i = 0; i < NU; ++i) last[i] = -1;
+      // block j of item x, keys or values, into ring unit u
+      auto load = [&](const Walker& x, int j, int kv, int u) -> bool {
+        const int32_t* bt = a.c.block_table + static_cast<int64_t>(x.b) * a.c.max_pages;
+        int id[2];
+        uint32_t bytes = 0;
+        for (int p = 0; p < 2; ++p) {
+          const int pg = (x.blk0 + j) * 2 + p;
+          id[p] = -1;
+          if (pg * kPg <= x.hi && pg * kPg + kPg - 1 >= x.lo) id[p] = bt[pg];
+          if (id[p] < 0 || id[p] >= a.c.num_pages) id[p] = -1;
+          else bytes += kPg * D;
+        }
+        const int s = u % NU;
+        if (u >= NU && !fwait(&u_empty[s], ((u / NU) - 1) & 1, a.c.status, fail)) return false;
+        mbar_arrive_expect_tx(&u_full[s], bytes);
+        for (int p = 0; p < 2; ++p) {
+          if (id[p] < 0) continue;
+          const int y = (id[p] * a.c.n_kv_heads + x.h) * kPg;
 #pragma unroll
-              for (int t = 0; t < ATOMS; ++t)
-                tma_load_2d(ring + s * C::kUnitBytes + t * kAtom + p * (kPg * 128), kv ? &tv : &tk, &u_full[s],
-                            t * 128, y, pol);
-            }
-            ++nu;
+          for (int t = 0; t < ATOMS; ++t)
+            tma_load_2d(ring + s * C::kUnitBytes + t * kAtom + p * (kPg * 128), kv ? &tv : &tk, &u_full[s], t * 128,
+                        y, pol);
+        }
+        last[s] = u;
+        return true;
+      };
+      Walker wk = w;
+      wk.skip();
+      w.skip();
+      int gk = 0, gv = 0, jk = 0, jv = 0, nq = 0, qy = -1;   // qy: first row of queries still to load
+      bool ok = true;
+      auto load_q = [&]() -> bool {
+        const int qb = nq % QB;
+        if (nq >= QB && !fwait(&q_empty[qb], ((nq / QB) - 1) & 1, a.c.status, fail)) return false;
+        mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
+        for (int c = 0; c < 2; ++c)
+          for (int t = 0; t < ATOMS; ++t)
+            for (int r = 0; r < 128; r += RP)
+              tma_load_2d(qbuf + qb * C::kQBytes + (c * ATOMS + t) * (128 * 128) + r * 128, &tq, &q_full[qb],
+                          t * 128, c * plane + qy, pol_q);
+        ++nq;
+        qy = -1;
+        return true;
+      };
+      // order of the copies: K0 K1 V0 K2 V1 ..: values are needed a softmax
+      // later than their keys, and would hold a slot meanwhile.  New queries
+      // wait for their buffer behind the values of the block before.
+      while (ok && w.valid()) {
+        while (ok && wk.valid() && gk < gv + 2) {
+          if (wk.fresh) {
+            qy = (wk.b * a.c.n_kv_heads + wk.h) * a.rows + wk.rb * RP;
+            wk.fresh = false;
           }
-          // new queries behind the item's first block: their buffer may still
-          // be in use, and that must not hold back the first copies
-          if (ok && w.fresh) {
-            const int qb = nq % QB;
-            if (nq >= QB && !(ok = fwait(&q_empty[qb], ((nq / QB) - 1) & 1, a.c.status, fail))) break;
-            mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
-            const int y = (w.b * a.c.n_kv_heads + w.h) * a.rows + w.rb * RP;
-            for (int c = 0; c < 2; ++c)
-              for (int t = 0; t < ATOMS; ++t)
-                for (int r = 0; r < 128; r += RP)
-                  tma_load_2d(qbuf + qb * C::kQBytes + (c * ATOMS + t) * (128 * 128) + r * 128, &tq, &q_full[qb],
-                              t * 128, c * plane + y, pol_q);
-            ++nq;
-            w.fresh = false;
+          ok = load(wk, jk, 0, key_unit(gk));
+          ++gk;
+          if (ok && gk == 1) ok = load_q();
+          if (++jk >= wk.nb) {
+            jk = 0;
+            wk.next();
+            wk.skip();
           }
+        }
+        ok = ok && load(w, jv, 1, value_unit(gv));
+        ++gv;
+        if (ok && qy >= 0) ok = load_q();
+        if (++jv >= w.nb) {
+          jv = 0;
+          w.next();
+          w.skip();
         }
       }
       // every issued copy must land before the CTA may exit
-      for (int i = (nu > NU ? nu - NU : 0); i < nu; ++i) mbar_wait(&u_full[i % NU], (i / NU) & 1, a.c.status);
+      for (int i = 0; i < NU; ++i)
+        if (last[i] >= 0) mbar_wait(&u_full[i], (last[i] / NU) & 1, a.c.status);
       for (int i = (nq > QB ? nq - QB : 0); i < nq; ++i) mbar_wait(&q_full[i % QB], (i / QB) & 1, a.c.status);
     }
   } else if (warp == 1) {
@@ -379,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     if (lane == 0) {
       const uint32_t id_qk = idesc_e4m3(kBlk, false), id_pv = idesc_e4m3(D, true);
       Walker wp = w;
-      while (w.valid() && w.nb == 0) w.next();
-      while (wp.valid() && wp.nb == 0) wp.next();
+      w.skip();
+      wp.skip();
       int js = 0, jp = 0, ip = 0;         // block in item (scores, P V); items begun by P V
       int nqk = 0, npv = 0, nq = 0;       // blocks issued; query groups begun
       bool waiting_q = false;
@@ -389,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       while (wp.valid()) {
         bool progressed = false;
         if (npv < nqk) {                  // P V first: it frees a unit
-          const int u = 2 * npv + 1;
+          const int u = value_unit(npv);
           bool ready = mbar_test_wait(&p_full[npv & 1], (npv >> 1) & 1) &&
                        mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
           if (jp == 0 && ip > 0) ready = ready && mbar_test_wait(o_free, (ip - 1) & 1);
@@ -407,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             if (++jp >= wp.nb) {
               jp = 0;
               ++ip;
-              do wp.next();
-              while (wp.valid() && wp.nb == 0);
+              wp.next();
+              wp.skip();
             }
             progressed = true;
           }
@@ -419,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             ++nq;
             waiting_q = true;
           }
-          const int u = 2 * nqk, qb = (nq - 1) % QB;
+          const int u = key_unit(nqk), qb = (nq - 1) % QB;
           bool ready = !waiting_q || mbar_test_wait(&q_full[qb], ((nq - 1) / QB) & 1);
           ready = ready && mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
           if (ready) {
@@ -440,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             ++nqk;
             if (++js >= w.nb) {
               js = 0;
-              do w.next();
-              while (w.valid() && w.nb == 0);
+              w.next();
+              w.skip();
             }
             progressed = true;
           }
@@ -507,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     constexpr int kRowThreads = RP == 64 ? 128 : 256;
     const int lg_bt = 31 - __clz(a.c.block);
     float* red_r = red + rh * (NG * 32);
-    int g = 0, item = 0;
+    int g = 0, item = 0, p = 0;
+    float qs = 0.f;
     for (; w.valid(); w.next()) {
       const int r0 = w.rb * RP, nrows = min(a.rows - r0, RP);
       const long bh = static_cast<long>(w.b) * a.c.n_kv_heads + w.h;
@@ -518,10 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       }
       const bool half_used = rh * 32 < nrows;         // these warps hold rows
       const bool mine = row < nrows;
-      const int p = w.L + a.q_offset + (r0 + row) / a.G;
+      if (w.fresh) {
+        w.fresh = false;
+        p = w.L + a.q_offset + (r0 + row) / a.G;
+        qs = mine ? a.q_scale[bh * a.rows + r0 + row] : 0.f;
+        qs = qs == qs ? qs * a.scale_log2 : 0.f;      // a NaN row's result is set at the end
+      }
       const int row_lo = max(w.lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(w.hi, p);
-      float qs = mine ? a.q_scale[bh * a.rows + r0 + row] : 0.f;
-      qs = qs == qs ? qs * a.scale_log2 : 0.f;        // a NaN row's result is set at the end
       const float* ks = ks_s + (item & 1) * kMaxScales;
       const float* vs = vs_s + (item & 1) * kMaxScales;
       fwait(&sc_full[item & 1], (item >> 1) & 1, a.c.status, fail);
@@ -640,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         {
           const int key = kb + (st >> 1);
           if (key < w.lo || key > w.hi || vs[((j << kLgBlk) + (st >> 1)) >> lg_bt] < 0.f) {
-            const int u = 2 * g + 1;
+            const int u = value_unit(g);
             fwait(&u_full[u % NU], (u / NU) & 1, a.c.status, fail);
             uint8_t* vrow = ring + (u % NU) * C::kUnitBytes + (st >> 1) * 128;
 #pragma unroll
@@ -681,15 +720,16 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
               for (int c = 0; c < 32; ++c) stage[c * 32 + lane] = o[c];
             }
             named_bar(bar_cg, 64);
-            if (quad < 2 && mine && !*fail) {
+            if (quad < 2) {
+              float low[32];
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                float4 v;
-                v.x = fmaf(stage[c * 32 + lane], 1.f / kLow, o[c]) * (1.f / kUnit);
-                v.y = fmaf(stage[c * 32 + 32 + lane], 1.f / kLow, o[c + 1]) * (1.f / kUnit);
-                v.z = fmaf(stage[c * 32 + 64 + lane], 1.f / kLow, o[c + 2]) * (1.f / kUnit);
-                v.w = fmaf(stage[c * 32 + 96 + lane], 1.f / kLow, o[c + 3]) * (1.f / kUnit);
-                __stcg(reinterpret_cast<float4*>(po + c0 + c), v);
+              for (int c = 0; c < 32; ++c) low[c] = stage[c * 32 + lane];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = fmaf(low[c], 1.f / kLow, o[c]) * (1.f / kUnit);
+              if (mine && !*fail) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                  __stcg(reinterpret_cast<float4*>(po + c0 + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
               }
             }
             named_bar(bar_cg, 64);
