@@ -6,26 +6,26 @@
 //
 // The cache is e4m3, so the products run in kind::f8f6f4 on the pages as TMA
 // brought them, with no conversion of K or V.  The bf16 side of each product is
-// held in two e4m3 codes whose sum keeps 8 bits: queries q = c0 + c1 (written
-// by the query kernel; two MMA passes into one accumulator) and weights p = w0 +
+// held in two e4m3 codes whose sum keeps 8 bits: queries q = c0 + c1 (from the
+// query kernel; in TMEM; two MMA passes into one accumulator) and weights p = w0 +
 // w1 / 16 (w1 the rounding error of w0, stacked under w0 in the M dimension, so
 // one pass gives both sums, in lanes r and 64 + r of the accumulator).
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
 // that start in an equal share of all key blocks.  11 warps:
-//   warp 0     TMA producer: keys, then values, of 128-key blocks (two pages)
-//              into a ring of kUnits units of 128 x dim bytes, and the queries,
-//              128 / RP copies of them one below the other in the tile.
+//   warp 0     TMA producer: keys and values of 128-key blocks (two pages) into
+//              a ring of kUnits units of 128 x dim bytes.
 //   warp 1     allocates TMEM; one thread issues the MMAs: S[128][128 keys] = Q
-//              K^T (A = Q, B = K, both K-major), two buffers; O[rows][dim] += P V
-//              (A = P, K-major, B = V as stored, MN-major).
+//              K^T (A = Q from TMEM, B = K, K-major); O[rows][dim] += P V (A = P
+//              in shared memory, K-major, B = V as stored, MN-major).  With Q in
+//              shared memory too the two operands took all of its bandwidth.
 //   warp 2     page ids -> the item's scales in shared memory, an item ahead.
-//   warps 3-10 softmax: a thread takes one query row and 128 / (256 / RP) of the
-//              block's keys.  The copies of the queries give every TMEM lane
-//              quadrant, and so every scheduler, an equal part of the keys
-//              (one copy in lanes 0..RP-1 left all of the work to one or two
-//              schedulers: 4300 clocks a block instead of TUNED).  A row's
+//   warps 3-10 softmax: a thread takes one query row and RP / 2 of the block's
+//              keys.  The queries sit 128 / RP times in the 128 lanes of Q, so
+//              every TMEM lane quadrant, and with it every scheduler, takes an
+//              equal part of the keys (one copy left all of the work to one or
+//              two schedulers, at 4300 clocks a block).  A row's
 //              reference m moves only when a block exceeds it by 2^kLazy (one
 //              barrier vote per block); the v scale is folded into m and p
 //              (p v_scale <= 2^kLazy), so blocks of any scale share one
@@ -82,6 +82,16 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with A in TMEM (lane = row, four K elements a column)
+__device__ __forceinline__ void umma_e4m3_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Instruction descriptor, kind::f8f6f4: D binary32, A and B e4m3, M = 128, N = n,
 // A K-major, B K-major or MN-major.
 __device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn) {
@@ -91,16 +101,17 @@ __device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn) {
 template <int D>
 struct Cfg {
   static constexpr uint32_t kUnitBytes = kBlk * D;              // one block's keys or values
-  static constexpr uint32_t kQBytes = 2u * 128u * D;            // [code][atom][128 rows][128 B]
-  // two P and query buffers where they leave room for the ring (dim 128)
   static constexpr int kPBufs = D == 128 ? 2 : 1;
-  static constexpr int kQBufs = D == 128 ? 2 : 1;
-  static constexpr int kUnits = D == 128 ? 7 : 4;
-  static constexpr uint32_t kOffP = kQBufs * kQBytes;
-  static constexpr uint32_t kOffRing = kOffP + kPBufs * kPBytes;
+  static constexpr int kUnits = D == 128 ? 11 : 6;
+  static constexpr uint32_t kOffRing = kPBufs * kPBytes;
   static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnitBytes;
   static constexpr uint32_t kSmem = 1024 + kOffTail + kTail;
   static_assert(kSmem <= kSmemMax, "shared memory");
+  // TMEM columns: output, scores, both codes of the queries (4 dims a column)
+  static constexpr int kSBufs = D == 128 ? 2 : 1;
+  static constexpr uint32_t kColS = D;
+  static constexpr uint32_t kColQ = kColS + kSBufs * kBlk;
+  static_assert(kColQ + 2 * D / 4 <= 512, "tensor memory");
 };
 
 // Keys any row of a sequence may see, as whole blocks; none: blocks = 0.
@@ -203,24 +214,21 @@ __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, unsigned* 
 template <int D, int RP>
 __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constant__ CUtensorMap tk,
                                                             const __grid_constant__ CUtensorMap tv,
-                                                            const __grid_constant__ CUtensorMap tq,
                                                             const __grid_constant__ QAttnArgs a) {
   using C = Cfg<D>;
-  constexpr int NU = C::kUnits, QB = C::kQBufs, PB = C::kPBufs, ATOMS = D / 128;
+  constexpr int NU = C::kUnits, PB = C::kPBufs, SB = C::kSBufs, ATOMS = D / 128;
   constexpr uint32_t kAtom = kBlk * 128;
-  constexpr uint32_t kColS = 256;            // score buffers behind the output's columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qbuf = smem;
-  uint8_t* pbuf = smem + C::kOffP;
+  uint8_t* pbuf = smem;
   uint8_t* ring = smem + C::kOffRing;
   uint8_t* tail = smem + C::kOffTail;
   uint64_t* u_full = reinterpret_cast<uint64_t*>(tail);   // [NU]
   uint64_t* u_empty = u_full + NU;                         // [NU]
-  uint64_t* q_full = u_empty + NU;                         // [2]
-  uint64_t* q_empty = q_full + 2;                          // [2]
-  uint64_t* s_full = q_empty + 2;                          // [2] by block parity
-  uint64_t* p_full = s_full + 2;                           // [2]
+  uint64_t* s_full = u_empty + NU;                         // [SB] by block
+  uint64_t* s_free = s_full + 2;                           // [SB]
+  uint64_t* q_ready = s_free + 2;
+  uint64_t* p_full = q_ready + 1;                          // [2] by block parity
   uint64_t* pv_done = p_full + 2;                          // [2]
   uint64_t* sc_full = pv_done + 2;                         // [2] by item parity
   uint64_t* sc_empty = sc_full + 2;                        // [2]
@@ -241,14 +249,14 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       mbar_init(&u_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kSoftWarps);
       mbar_init(&p_full[i], kSoftWarps);
       mbar_init(&pv_done[i], 1);
       mbar_init(&sc_full[i], 1);
       mbar_init(&sc_empty[i], kSoftWarps);
     }
+    mbar_init(q_ready, kSoftWarps);
     mbar_init(o_free, kSoftWarps);
     mbar_init(mma_done, 1);
     *fail = 0;
@@ -257,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
-    prefetch_tmap(&tq);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_trigger();
@@ -329,8 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol = RB > 1 ? policy_evict_normal() : policy_evict_first();
-      const uint64_t pol_q = policy_evict_normal();
-      const int plane = a.B * a.c.n_kv_heads * a.rows;
       int last[NU];                       // unit last copied into each slot, -1: none
       for (int i = 0; i < NU; ++i) last[i] = -1;
       // block j of item x, keys or values, into ring unit u
@@ -362,33 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       Walker wk = w;
       wk.skip();
       w.skip();
-      int gk = 0, gv = 0, jk = 0, jv = 0, nq = 0, qy = -1;   // qy: first row of queries still to load
+      int gk = 0, gv = 0, jk = 0, jv = 0;
       bool ok = true;
-      auto load_q = [&]() -> bool {
-        const int qb = nq % QB;
-        if (nq >= QB && !fwait(&q_empty[qb], ((nq / QB) - 1) & 1, a.c.status, fail)) return false;
-        mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
-        for (int c = 0; c < 2; ++c)
-          for (int t = 0; t < ATOMS; ++t)
-            for (int r = 0; r < 128; r += RP)
-              tma_load_2d(qbuf + qb * C::kQBytes + (c * ATOMS + t) * (128 * 128) + r * 128, &tq, &q_full[qb],
-                          t * 128, c * plane + qy, pol_q);
-        ++nq;
-        qy = -1;
-        return true;
-      };
       // order of the copies: K0 K1 V0 K2 V1 ..: values are needed a softmax
-      // later than their keys, and would hold a slot meanwhile.  New queries
-      // wait for their buffer behind the values of the block before.
+      // later than their keys, and would hold a slot meanwhile
       while (ok && w.valid()) {
         while (ok && wk.valid() && gk < gv + 2) {
-          if (wk.fresh) {
-            qy = (wk.b * a.c.n_kv_heads + wk.h) * a.rows + wk.rb * RP;
-            wk.fresh = false;
-          }
           ok = load(wk, jk, 0, key_unit(gk));
           ++gk;
-          if (ok && gk == 1) ok = load_q();
           if (++jk >= wk.nb) {
             jk = 0;
             wk.next();
@@ -397,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         }
         ok = ok && load(w, jv, 1, value_unit(gv));
         ++gv;
-        if (ok && qy >= 0) ok = load_q();
         if (++jv >= w.nb) {
           jv = 0;
           w.next();
@@ -407,7 +392,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       // every issued copy must land before the CTA may exit
       for (int i = 0; i < NU; ++i)
         if (last[i] >= 0) mbar_wait(&u_full[i], (last[i] / NU) & 1, a.c.status);
-      for (int i = (nq > QB ? nq - QB : 0); i < nq; ++i) mbar_wait(&q_full[i % QB], (i / QB) & 1, a.c.status);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue
@@ -418,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       wp.skip();
       int js = 0, jp = 0, ip = 0;         // block in item (scores, P V); items begun by P V
       int nqk = 0, npv = 0, nq = 0;       // blocks issued; query groups begun
-      bool waiting_q = false;
       uint64_t t_last = 0;
       uint32_t polls = 0;
       while (wp.valid()) {
@@ -448,29 +431,24 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             progressed = true;
           }
         }
-        if (w.valid() && nqk <= npv + 1) {
-          if (js == 0 && w.fresh && !waiting_q) {
-            if (nq > 0) umma_commit(&q_empty[(nq - 1) % QB]);   // the last group's scores are issued
-            ++nq;
-            waiting_q = true;
-          }
-          const int u = key_unit(nqk), qb = (nq - 1) % QB;
-          bool ready = !waiting_q || mbar_test_wait(&q_full[qb], ((nq - 1) / QB) & 1);
-          ready = ready && mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
+        if (w.valid()) {
+          const int u = key_unit(nqk);
+          bool ready = mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
+          if (nqk >= SB) ready = ready && mbar_test_wait(&s_free[nqk % SB], ((nqk / SB) - 1) & 1);
+          if (w.fresh) ready = ready && mbar_test_wait(q_ready, nq & 1);
           if (ready) {
-            waiting_q = false;
+            if (w.fresh) ++nq;
             w.fresh = false;
             tc_fence_after();
             const uint32_t k_addr = smem_u32(ring + (u % NU) * C::kUnitBytes);
-            const uint32_t q_addr = smem_u32(qbuf + qb * C::kQBytes);
-            const uint32_t t_s = tmem + kColS + (nqk & 1) * kBlk;
+            const uint32_t t_s = tmem + C::kColS + (nqk % SB) * kBlk;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                umma_e4m3(t_s, sw128_desc(q_addr + (c * ATOMS + (kk >> 2)) * (128 * 128) + (kk & 3) * 32),
-                          sw128_desc(k_addr + (kk >> 2) * kAtom + (kk & 3) * 32), id_qk, (c > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&s_full[nqk & 1]);
+                umma_e4m3_ta(t_s, tmem + C::kColQ + c * (D / 4) + kk * 8,
+                             sw128_desc(k_addr + (kk >> 2) * kAtom + (kk & 3) * 32), id_qk, (c > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&s_full[nqk % SB]);
             umma_commit(&u_empty[u % NU]);
             ++nqk;
             if (++js >= w.nb) {
@@ -544,22 +522,52 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     float* red_r = red + rh * (NG * 32);
     int g = 0, item = 0, p = 0;
     float qs = 0.f;
-    for (; w.valid(); w.next()) {
-      const int r0 = w.rb * RP, nrows = min(a.rows - r0, RP);
-      const long bh = static_cast<long>(w.b) * a.c.n_kv_heads + w.h;
-      const long slot = (bh * a.n_splits + w.sidx) * a.rows + r0;
-      if (w.nb == 0) {
-        if (grp == 0 && row < nrows) __stcg(&a.part_ml[slot + row], make_float2(kNoKey, 0.f));
-        continue;
+    // To the next item with keys (the partials of those without go out here);
+    // where the queries change, this thread's row of them into TMEM: every
+    // product with the old ones is done once the last scores have been read.
+    auto take = [&]() {
+      for (; w.valid() && w.nb == 0; w.next()) {
+        const int r0 = w.rb * RP;
+        const long slot = ((static_cast<long>(w.b) * a.c.n_kv_heads + w.h) * a.n_splits + w.sidx) * a.rows + r0;
+        if (grp == 0 && row < min(a.rows - r0, RP)) __stcg(&a.part_ml[slot + row], make_float2(kNoKey, 0.f));
       }
+      if (!w.valid() || !w.fresh) return;
+      w.fresh = false;
+      const int r0 = w.rb * RP;
+      const bool have = row < min(a.rows - r0, RP);
+      const long at = (static_cast<long>(w.b) * a.c.n_kv_heads + w.h) * a.rows + r0 + row;
+      p = w.L + a.q_offset + (r0 + row) / a.G;
+      qs = have ? a.q_scale[at] : 0.f;
+      qs = qs == qs ? qs * a.scale_log2 : 0.f;        // a NaN row's result is set at the end
+      const long plane = static_cast<long>(a.B) * a.c.n_kv_heads * a.rows;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q_codes + (at + c * plane) * D + cg * (D / 2));
+        uint32_t v[D / 32][4];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 x = have ? __ldcg(src + i) : make_uint4(0, 0, 0, 0);
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+          v[i][2] = x.z;
+          v[i][3] = x.w;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          tmem_st8(t_lane + C::kColQ + c * (D / 4) + cg * (D / 8) + i * 8, *reinterpret_cast<uint32_t(*)[8]>(v[2 * i]));
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    };
+    take();
+    while (w.valid()) {
+      const int r0 = w.rb * RP, nrows = min(a.rows - r0, RP);
+      const long slot = ((static_cast<long>(w.b) * a.c.n_kv_heads + w.h) * a.n_splits + w.sidx) * a.rows + r0;
       const bool half_used = rh * 32 < nrows;         // these warps hold rows
       const bool mine = row < nrows;
-      if (w.fresh) {
-        w.fresh = false;
-        p = w.L + a.q_offset + (r0 + row) / a.G;
-        qs = mine ? a.q_scale[bh * a.rows + r0 + row] : 0.f;
-        qs = qs == qs ? qs * a.scale_log2 : 0.f;      // a NaN row's result is set at the end
-      }
       const int row_lo = max(w.lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(w.hi, p);
       const float* ks = ks_s + (item & 1) * kMaxScales;
       const float* vs = vs_s + (item & 1) * kMaxScales;
@@ -575,14 +583,19 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           vsc[u] = vs[e];
           f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), 3e38f);
         }
-        fwait(&s_full[g & 1], (g >> 1) & 1, a.c.status, fail);
+        fwait(&s_full[g % SB], (g / SB) & 1, a.c.status, fail);
         __syncwarp();
         tc_fence_after();
         if (half_used) {
-          const uint32_t t_s = t_lane + kColS + (g & 1) * kBlk + grp * KW;
+          const uint32_t t_s = t_lane + C::kColS + (g % SB) * kBlk + grp * KW;
 #pragma unroll
           for (int c = 0; c < KW; c += 8) tmem_ld8_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[8]>(&s[c]));
           tmem_ld_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[g % SB]);
+        if (half_used) {
           bool edge = key0 < row_lo || key0 + KW - 1 > row_hi;
 #pragma unroll
           for (int u = 0; u < NE; ++u) edge |= vsc[u] < 0.f;
@@ -694,9 +707,12 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
-      // ---- the item's (m, l) and o = (o0 + o1 / 16) / kUnit: the lanes of w1's
-      // sums pass theirs through shared memory (this row half's part of the P
-      // buffer, which no MMA reads now)
+      // ---- on to the next item's queries, then this one's (m, l) and o = (o0 +
+      // o1 / 16) / kUnit: quadrants 0, 1 hold o0 and 2, 3 o1; each finishes half
+      // of the columns and passes its sums of the others through shared memory
+      // (this row half's part of the P buffer, which no MMA reads now)
+      w.next();
+      take();
       fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
       __syncwarp();
       tc_fence_after();
@@ -709,28 +725,34 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           sum += (red_r[e * 32 + lane] + red_r[e * 32 + 32 + lane]) + (red_r[e * 32 + 64 + lane] + red_r[e * 32 + 96 + lane]);
         if (grp == 0 && mine && !*fail) __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
         if (sums) {
-          float* stage = reinterpret_cast<float*>(pbuf + (64 * cg + 32 * rh) * 128);
+          constexpr int CW = RP == 32 ? 32 : 16;       // columns a warp finishes at a time
+          const bool low = quad >= 2;
+          float* give = reinterpret_cast<float*>(pbuf + (64 * cg + 32 * rh) * 128) + (low ? 0 : CW * 32) + lane;
+          const float* get = reinterpret_cast<const float*>(pbuf + (64 * cg + 32 * rh) * 128) + (low ? CW * 32 : 0) + lane;
           float* po = a.part_o + (slot + row) * D;
 #pragma unroll 1
-          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 32) {
-            float o[32];
-            tmem_ld32(t_lane + c0, o);
-            if (quad >= 2) {
+          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 2 * CW) {
+            const int mine0 = c0 + (low ? CW : 0), other0 = c0 + (low ? 0 : CW);
+            uint32_t o[CW / 8][8], x[CW / 8][8];
 #pragma unroll
-              for (int c = 0; c < 32; ++c) stage[c * 32 + lane] = o[c];
+            for (int c = 0; c < CW / 8; ++c) {
+              tmem_ld8_nowait(t_lane + mine0 + 8 * c, o[c]);
+              tmem_ld8_nowait(t_lane + other0 + 8 * c, x[c]);
             }
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < CW; ++c) give[c * 32] = __uint_as_float(x[c >> 3][c & 7]);
             named_bar(bar_cg, 64);
-            if (quad < 2) {
-              float low[32];
+            float y[CW];
+            const float f_own = low ? 1.f / (kUnit * kLow) : 1.f / kUnit, f_get = low ? 1.f / kUnit : 1.f / (kUnit * kLow);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) low[c] = stage[c * 32 + lane];
+            for (int c = 0; c < CW; ++c) y[c] = get[c * 32];
 #pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = fmaf(low[c], 1.f / kLow, o[c]) * (1.f / kUnit);
-              if (mine && !*fail) {
+            for (int c = 0; c < CW; ++c) y[c] = fmaf(y[c], f_get, __uint_as_float(o[c >> 3][c & 7]) * f_own);
+            if (mine && !*fail) {
 #pragma unroll
-                for (int c = 0; c < 32; c += 4)
-                  __stcg(reinterpret_cast<float4*>(po + c0 + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
-              }
+              for (int c = 0; c < CW; c += 4)
+                __stcg(reinterpret_cast<float4*>(po + mine0 + c), make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]));
             }
             named_bar(bar_cg, 64);
           }
@@ -811,20 +833,20 @@ __global__ void __launch_bounds__(128) qattn_combine_kernel(const __grid_constan
 }
 
 template <int D, int RP>
-cudaError_t launch_one(int grid, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+cudaError_t launch_one(int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                        const QAttnArgs& a, cudaStream_t st) {
   auto kern = qattn_kernel<D, RP>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, tk, tv, tq, a);
+  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, tk, tv, a);
 }
 
 template <int D>
-cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                        const QAttnArgs& a, cudaStream_t st) {
-  if (rp == 32) return launch_one<D, 32>(grid, tk, tv, tq, a, st);
-  return launch_one<D, 64>(grid, tk, tv, tq, a, st);
+  if (rp == 32) return launch_one<D, 32>(grid, tk, tv, a, st);
+  return launch_one<D, 64>(grid, tk, tv, a, st);
 }
 
 }  // namespace
@@ -832,10 +854,8 @@ cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMa
 cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   const int D = a.c.dim, rp = a.rows <= 32 ? 32 : 64;
   const uint64_t rows = static_cast<uint64_t>(a.c.num_pages) * a.c.n_kv_heads * kPg;
-  const uint64_t qrows = 2ull * a.B * a.c.n_kv_heads * a.rows;
-  CUtensorMap tk, tv, tq;
-  if (!make_tmap_u8_2d(&tk, a.c.k, rows, D, kPg, 128) || !make_tmap_u8_2d(&tv, a.c.v, rows, D, kPg, 128) ||
-      !make_tmap_u8_2d(&tq, a.q_codes, qrows, D, rp, 128))
+  CUtensorMap tk, tv;
+  if (!make_tmap_u8_2d(&tk, a.c.k, rows, D, kPg, 128) || !make_tmap_u8_2d(&tv, a.c.v, rows, D, kPg, 128))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -843,7 +863,7 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rp - 1) / rp) * a.n_splits;
   const int grid = static_cast<int>(items < sms ? items : sms);
-  e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, tq, a, st) : launch_dim<128>(rp, grid, tk, tv, tq, a, st);
+  e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   return launch_k(qattn_combine_kernel, dim3(a.B * a.c.n_kv_heads * a.rows), dim3(128), 0, st, a);
 }
