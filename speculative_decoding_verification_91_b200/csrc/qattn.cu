@@ -13,15 +13,17 @@
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
-// that start in an equal share of all key blocks.  11 warps:
+// that start in an equal share of all key blocks.  12 warps:
 //   warp 0     TMA producer: keys and values of 128-key blocks (two pages) into
 //              a ring of kUnits units of 128 x dim bytes.
-//   warp 1     allocates TMEM; one thread issues the MMAs: S[128][128 keys] = Q
-//              K^T (A = Q from TMEM, B = K, K-major); O[rows][dim] += P V (A = P
-//              in shared memory, K-major, B = V as stored, MN-major).  With Q in
-//              shared memory too the two operands took all of its bandwidth.
-//   warp 2     page ids -> the item's scales in shared memory, an item ahead.
-//   warps 3-10 softmax: a thread takes one query row and RP / 2 of the block's
+//   warp 1     allocates TMEM; one thread issues S[128][128 keys] = Q K^T (A = Q
+//              from TMEM, B = K, K-major).  With Q in shared memory too the two
+//              operands took all of its bandwidth.
+//   warp 2     finds the CTA's items and describes them in shared memory, with
+//              their scales, up to kItems ahead.
+//   warp 3     one thread issues O[rows][dim] += P V (A = P in shared memory,
+//              K-major, B = V as stored, MN-major).
+//   warps 4-11 softmax: a thread takes one query row and RP / 2 of the block's
 //              keys.  The queries sit 128 / RP times in the 128 lanes of Q, so
 //              every TMEM lane quadrant, and with it every scheduler, takes an
 //              equal part of the keys (one copy left all of the work to one or
@@ -48,14 +50,15 @@ namespace sv {
 
 namespace {
 
-constexpr int kBlk = 128;                  // keys per block
+constexpr int kBlk = kQBlk;                // keys per block
 constexpr int kLgBlk = 7;
 constexpr int kPg = SPEC_PAGE_SIZE;
 constexpr int kSoftWarps = 8;
-constexpr int kFirstSoft = 3;
+constexpr int kFirstSoft = 4;
 constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
 constexpr uint32_t kSmemMax = 227u * 1024u;
-constexpr uint32_t kTail = 8192;
+constexpr int kItems = 4;                  // items described ahead in shared memory
+constexpr uint32_t kTail = 12288;
 constexpr uint32_t kPBytes = 128 * kBlk;   // w0 rows 0..63, w1 rows 64..127
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
 // p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448.  A larger
@@ -114,22 +117,18 @@ struct Cfg {
   static_assert(kColQ + 2 * D / 4 <= 512, "tensor memory");
 };
 
-// Keys any row of a sequence may see, as whole blocks; none: blocks = 0.
-struct SeqKeys {
-  int lo, hi, splits, blocks;
+// One work item as the roles see it; nb < 0: the end.
+struct Item {
+  int h, r0, nrows, p0;    // KV head, first row of the block, its rows, the sequence's first position
+  int lo, hi, blk0, nb;    // its keys and blocks
+  int fresh, pad;          // the queries differ from the item before
+  long slot;               // partial of its first row
+  long q_row;              // row of its first query among all
+  long page0;              // the sequence's block-table row
+  long out0;               // row of the sequence's first result
 };
-__device__ __forceinline__ SeqKeys seq_keys(const QAttnArgs& a, int L) {
-  SeqKeys k{0, -1, 0, 0};
-  if (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * kPg) return k;
-  k.hi = min(L + a.kv_extra - 1, L + a.q_offset + a.n - 1);
-  k.lo = a.window > 0 ? max(0, L + a.q_offset - a.window + 1) : 0;
-  if (k.hi < k.lo) return k;
-  k.splits = k.hi / a.split - k.lo / a.split + 1;
-  k.blocks = k.hi / kBlk - k.lo / kBlk + 1;
-  return k;
-}
 
-// Walks the items of one CTA; every role keeps its own.
+// Walks the items of one CTA.
 struct Walker {
   const QAttnArgs* a;
   int RP, RB;              // rows of a block, row blocks
@@ -138,20 +137,21 @@ struct Walker {
   SeqKeys k;
   long base, end, pos;     // key blocks before (b, h, rb); where the CTA stops; this item's start
   int lo, hi, blk0, nb;    // this item's keys and blocks (nb = 0: none)
-  bool fresh;              // the queries changed since the role last took them
+  bool fresh;
   __device__ bool valid() const { return b < a->B && pos < end; }
   __device__ void load_seq() {
     L = a->c.seq_lens[b];
     k = seq_keys(*a, L);
     split0 = k.lo / a->split;
   }
-  __device__ void load_rows() {
-    const int r0 = rb * RP, r1 = min(a->rows, r0 + RP) - 1;
-    p0 = L + a->q_offset + r0 / a->G;
-    p1 = L + a->q_offset + r1 / a->G;
-    fresh = true;
-  }
-  __device__ void derive() {
+  // from the first split of (b, h, rb) that is wanted: its rows, then its keys
+  __device__ void derive(bool rows) {
+    if (rows) {
+      const int r0 = rb * RP, r1 = min(a->rows, r0 + RP) - 1;
+      p0 = L + a->q_offset + r0 / a->G;
+      p1 = L + a->q_offset + r1 / a->G;
+      fresh = true;
+    }
     const int s0 = (split0 + sidx) * a->split, start = max(s0, k.lo);
     pos = base + ((start >> kLgBlk) - (k.lo >> kLgBlk));
     lo = a->window > 0 ? max(start, p0 - a->window + 1) : start;
@@ -159,44 +159,24 @@ struct Walker {
     blk0 = lo >> kLgBlk;
     nb = hi >= lo ? (hi >> kLgBlk) - blk0 + 1 : 0;
   }
-  __device__ void next_rows() {   // the next (b, h, rb) that has keys, its first split
-    sidx = 0;
-    base += k.blocks;
-    if (++rb == RB) {
-      rb = 0;
-      if (++h == a->c.n_kv_heads) {
-        h = 0;
-        do {
-          if (++b >= a->B) return;
-          load_seq();
-        } while (k.blocks == 0);
+  __device__ void next() {
+    bool rows = false;
+    if (++sidx >= k.splits) {     // the next (b, h, rb) that has keys
+      rows = true;
+      sidx = 0;
+      base += k.blocks;
+      if (++rb == RB) {
+        rb = 0;
+        if (++h == a->c.n_kv_heads) {
+          h = 0;
+          do {
+            if (++b >= a->B) return;
+            load_seq();
+          } while (k.blocks == 0);
+        }
       }
     }
-    load_rows();
-    derive();
-  }
-  __device__ void next() {
-    if (++sidx < k.splits) derive();
-    else next_rows();
-  }
-  __device__ void skip() {   // to the next item with keys
-    while (valid() && nb == 0) next();
-  }
-  __device__ void start(const QAttnArgs* args, int rp, const int* at, long base0, long end0) {
-    a = args;
-    RP = rp;
-    RB = (a->rows + RP - 1) / RP;
-    b = at[0];
-    end = end0;
-    if (b >= a->B) return;
-    load_seq();
-    h = at[1] / RB;
-    rb = at[1] % RB;
-    sidx = at[2];
-    base = base0 + static_cast<long>(at[1]) * k.blocks;
-    load_rows();
-    if (sidx < k.splits) derive();
-    else next_rows();
+    derive(rows);
   }
 };
 
@@ -204,11 +184,24 @@ struct Walker {
 __device__ __forceinline__ int key_unit(int g) { return g == 0 ? 0 : 2 * g - 1; }
 __device__ __forceinline__ int value_unit(int g) { return 2 * g + 2; }
 
+// Bounded wait that gives up at once after a timeout anywhere in the CTA.  The
+// part past the first test is kept out of line: inlined at every wait (and with
+// a walker in every role) the kernel had 200 KB of code, and its roles spent
+// half of their time on instruction fetches.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* fail) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (*fail) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitNs) {
+      flag_status(status, SPEC_DEV_TIMEOUT);
+      *fail = 1;
+      return false;
+    }
+  }
+}
 __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* fail) {
-  if (*fail) return false;
-  if (mbar_wait(bar, parity, status)) return true;
-  *fail = 1;
-  return false;
+  return mbar_try_wait(bar, parity) || wait_more(bar, parity, status, fail);
 }
 
 template <int D, int RP>
@@ -227,21 +220,21 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   uint64_t* u_empty = u_full + NU;                         // [NU]
   uint64_t* s_full = u_empty + NU;                         // [SB] by block
   uint64_t* s_free = s_full + 2;                           // [SB]
-  uint64_t* q_ready = s_free + 2;
-  uint64_t* p_full = q_ready + 1;                          // [2] by block parity
+  uint64_t* p_full = s_free + 2;                           // [2] by block parity
   uint64_t* pv_done = p_full + 2;                          // [2]
-  uint64_t* sc_full = pv_done + 2;                         // [2] by item parity
-  uint64_t* sc_empty = sc_full + 2;                        // [2]
-  uint64_t* o_free = sc_empty + 2;
+  uint64_t* it_full = pv_done + 2;                         // [kItems] by item
+  uint64_t* it_empty = it_full + kItems;                   // [kItems]
+  uint64_t* q_ready = it_empty + kItems;
+  uint64_t* o_free = q_ready + 1;
   uint64_t* mma_done = o_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* at = reinterpret_cast<int*>(tmem_slot + 2);         // first item: b, (head, row block), split
-  long* span = reinterpret_cast<long*>(tail + 512);        // key blocks before it, and where to stop
+  Item* items = reinterpret_cast<Item*>(tail + 512);       // [kItems]
   float* red = reinterpret_cast<float*>(tail + 1024);      // [threads of a row][rows]
-  float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [2 items][kMaxScales]
-  float* vs_s = ks_s + 2 * kMaxScales;                     // < 0: page not there
+  float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [kItems][kMaxScales]
+  float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(sizeof(Item) * kItems <= 512, "items");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NU; ++i) {
@@ -253,12 +246,15 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       mbar_init(&s_free[i], kSoftWarps);
       mbar_init(&p_full[i], kSoftWarps);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&sc_full[i], 1);
-      mbar_init(&sc_empty[i], kSoftWarps);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], kSoftWarps + 2);
     }
     mbar_init(q_ready, kSoftWarps);
     mbar_init(o_free, kSoftWarps);
-    mbar_init(mma_done, 1);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     *fail = 0;
     fence_barrier_init();
   }
@@ -270,9 +266,141 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   pdl_trigger();
   pdl_wait();
 
-  const int RB = (a.rows + RP - 1) / RP, per_b = a.c.n_kv_heads * RB;
-  if (warp == 2) {
-    // ---- this CTA's share [x0, x1) of all key blocks and its first item
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return fwait(bar, parity, a.c.status, fail); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      // keys shared by several row blocks: normal priority in L2
+      const uint64_t pol = a.rows > RP ? policy_evict_normal() : policy_evict_first();
+      int gk = 0, gv = 0, jk = 0, jv = 0, ik = 0, iv = 0;   // blocks, block in item, item: of keys, of values
+      bool ok = true, more = true;                          // more: there may be keys left
+      // order of the copies: K0 K1 V0 K2 V1 ..: values are needed a softmax
+      // later than their keys, and would hold a slot meanwhile
+      for (;;) {
+        const bool key = more && gk < gv + 2;
+        if (!key && gv == gk) break;
+        const int i = key ? ik : iv, j = key ? jk : jv, u = key ? key_unit(gk) : value_unit(gv), s = u % NU;
+        if (key && j == 0 && !(ok = wait(&it_full[i % kItems], (i / kItems) & 1))) break;
+        const Item& x = items[i % kItems];
+        if (x.nb < 0) {
+          more = false;
+          continue;
+        }
+        const int32_t* bt = a.c.block_table + x.page0;
+        int y[2];
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int pg = (x.blk0 + j) * 2 + p;
+          int id = -1;
+          if (pg * kPg <= x.hi && pg * kPg + kPg - 1 >= x.lo) id = bt[pg];
+          const bool there = id >= 0 && id < a.c.num_pages;
+          y[p] = there ? (id * a.c.n_kv_heads + x.h) * kPg : -1;
+          if (there) bytes += kPg * D;
+        }
+        if (u >= NU && !(ok = wait(&u_empty[s], ((u / NU) - 1) & 1))) break;
+        mbar_arrive_expect_tx(&u_full[s], bytes);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if (y[p] >= 0)
+#pragma unroll
+            for (int t = 0; t < ATOMS; ++t)
+              tma_load_2d(ring + s * C::kUnitBytes + t * kAtom + p * (kPg * 128), key ? &tk : &tv, &u_full[s], t * 128,
+                          y[p], pol);
+        if (key) {
+          ++gk;
+          if (++jk == x.nb) jk = 0, ++ik;
+        } else {
+          ++gv;
+          if (++jv == x.nb) {
+            jv = 0;
+            mbar_arrive(&it_empty[iv % kItems]);
+            ++iv;
+          }
+        }
+      }
+      // every issued copy must land before the CTA may exit (a slot's last unit)
+      for (int i = 0; i < NU; ++i) {
+        int last = -1;
+        for (int g = max(0, gk - NU); g < gk; ++g)
+          if (key_unit(g) % NU == i) last = max(last, key_unit(g));
+        for (int g = max(0, gv - NU); g < gv; ++g)
+          if (value_unit(g) % NU == i) last = max(last, value_unit(g));
+        if (last >= 0) mbar_wait(&u_full[i], (last / NU) & 1, a.c.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- scores
+    if (lane == 0) {
+      const uint32_t id_qk = idesc_e4m3(kBlk, false);
+      int s = 0, su = 0, g = 0, nq = 0;     // ring slot and its round, block, query groups begun
+      for (int i = 0;; ++i) {
+        if (!wait(&it_full[i % kItems], (i / kItems) & 1)) break;
+        const int nb = items[i % kItems].nb;
+        bool ok = nb >= 0 && (!items[i % kItems].fresh || wait(q_ready, nq++ & 1));
+        for (int j = 0; ok && j < nb; ++j, ++g) {
+          ok = (g < SB || wait(&s_free[g % SB], ((g / SB) - 1) & 1)) && wait(&u_full[s], su & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_addr = smem_u32(ring + s * C::kUnitBytes);
+          const uint32_t t_s = tmem + C::kColS + (g % SB) * kBlk;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_e4m3_ta(t_s, tmem + C::kColQ + c * (D / 4) + kk * 8,
+                           sw128_desc(k_addr + (kk >> 2) * kAtom + (kk & 3) * 32), id_qk, (c > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&s_full[g % SB]);
+          umma_commit(&u_empty[s]);
+          s += g == 0 ? 1 : 2;              // K0 K1 V0 K2 V1 ..
+          if (s >= NU) s -= NU, ++su;
+        }
+        if (!ok) break;
+      }
+      umma_commit(&mma_done[0]);            // nothing may be in flight when TMEM is freed
+      mbar_wait(&mma_done[0], 0, a.c.status);
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- P V
+    // (a thread of its own: one thread that issued both spent 600 clocks from
+    // the last MMA of one product to the first of the other)
+    if (lane == 0) {
+      const uint32_t id_pv = idesc_e4m3(D, true);
+      int s = 2, su = 0, g = 0;
+      for (int i = 0;; ++i) {
+        if (!wait(&it_full[i % kItems], (i / kItems) & 1)) break;
+        const int nb = items[i % kItems].nb;
+        bool ok = nb >= 0 && (i == 0 || wait(o_free, (i - 1) & 1));
+        for (int j = 0; ok && j < nb; ++j, ++g) {
+          ok = wait(&u_full[s], su & 1) && wait(&p_full[g & 1], (g >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_addr = smem_u32(ring + s * C::kUnitBytes);
+          const uint32_t p_addr = smem_u32(pbuf + (g % PB) * kPBytes);
+#pragma unroll
+          for (int kk = 0; kk < kBlk / 32; ++kk)
+            umma_e4m3(tmem, sw128_desc(p_addr + kk * 32), sw128_desc_mn(v_addr + kk * 4096, kAtom), id_pv,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&pv_done[g & 1]);
+          umma_commit(&u_empty[s]);
+          s += 2;
+          if (s >= NU) s -= NU, ++su;
+        }
+        if (!ok) break;
+        mbar_arrive(&it_empty[i % kItems]);
+      }
+      umma_commit(&mma_done[1]);
+      mbar_wait(&mma_done[1], 0, a.c.status);
+    }
+  } else if (warp == 2) {
+    // --------------------------------------------------- items and scales
+    const int RB = (a.rows + RP - 1) / RP, per_b = a.c.n_kv_heads * RB;
+    // this CTA's share [x0, x1) of all key blocks and its first item
     long total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       long n = 0;
@@ -289,10 +417,14 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     }
     const long x0 = static_cast<long>(blockIdx.x) * total / gridDim.x;
     const long x1 = static_cast<long>(blockIdx.x + 1) * total / gridDim.x;
+    Walker w{};
+    w.a = &a;
+    w.RP = RP;
+    w.RB = RB;
+    w.b = a.B;
+    w.end = x1;
     long pre = 0;
-    int found = a.B;
-    long found_pre = 0;
-    for (int b0 = 0; b0 < a.B && found == a.B && x1 > x0; b0 += 32) {
+    for (int b0 = 0; b0 < a.B && w.b == a.B && x1 > x0; b0 += 32) {
       long n = 0;
       if (b0 + lane < a.B) n = static_cast<long>(seq_keys(a, a.c.seq_lens[b0 + lane]).blocks) * per_b;
       long incl = n;
@@ -305,204 +437,91 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const unsigned bal = __ballot_sync(0xffffffffu, n > 0 && x0 >= excl && x0 < excl + n);
       if (bal) {
         const int src = __ffs(bal) - 1;
-        found = b0 + src;
-        found_pre = __shfl_sync(0xffffffffu, excl, src);
+        w.b = b0 + src;
+        w.base = __shfl_sync(0xffffffffu, excl, src);
       }
       pre += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) {
-      at[0] = found;
-      at[1] = at[2] = 0;
-      span[0] = found_pre;
-      span[1] = x1;
-      if (found < a.B) {
-        const SeqKeys k = seq_keys(a, a.c.seq_lens[found]);
-        const long rem = x0 - found_pre;
-        at[1] = static_cast<int>(rem / k.blocks);
-        const int r = static_cast<int>(rem % k.blocks), first = k.lo / kBlk, bps = a.split / kBlk;
-        // the first split that starts at or after block r of the sequence
-        at[2] = r == 0 ? 0 : (r + first + bps - 1) / bps - k.lo / a.split;
+    if (w.b < a.B) {
+      w.load_seq();
+      const long rem = x0 - w.base;
+      const int hr = static_cast<int>(rem / w.k.blocks), r = static_cast<int>(rem % w.k.blocks);
+      w.h = hr / RB;
+      w.rb = hr % RB;
+      w.base += static_cast<long>(hr) * w.k.blocks;
+      // the first split that starts at or after block r of the sequence
+      const int first = w.k.lo >> kLgBlk, bps = a.split >> kLgBlk;
+      w.sidx = r == 0 ? 0 : (r + first + bps - 1) / bps - w.split0;
+      if (w.sidx < w.k.splits) {
+        w.derive(true);
+      } else {
+        w.sidx = w.k.splits - 1;
+        w.fresh = true;
+        w.next();
       }
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  Walker w;
-  w.start(&a, RP, at, span[0], span[1]);
-
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol = RB > 1 ? policy_evict_normal() : policy_evict_first();
-      int last[NU];                       // unit last copied into each slot, -1: none
-      for (int i = 0; i < NU; ++i) last[i] = -1;
-      // block j of item x, keys or values, into ring unit u
-      auto load = [&](const Walker& x, int j, int kv, int u) -> bool {
-        const int32_t* bt = a.c.block_table + static_cast<int64_t>(x.b) * a.c.max_pages;
-        int id[2];
-        uint32_t bytes = 0;
-        for (int p = 0; p < 2; ++p) {
-          const int pg = (x.blk0 + j) * 2 + p;
-          id[p] = -1;
-          if (pg * kPg <= x.hi && pg * kPg + kPg - 1 >= x.lo) id[p] = bt[pg];
-          if (id[p] < 0 || id[p] >= a.c.num_pages) id[p] = -1;
-          else bytes += kPg * D;
-        }
-        const int s = u % NU;
-        if (u >= NU && !fwait(&u_empty[s], ((u / NU) - 1) & 1, a.c.status, fail)) return false;
-        mbar_arrive_expect_tx(&u_full[s], bytes);
-        for (int p = 0; p < 2; ++p) {
-          if (id[p] < 0) continue;
-          const int y = (id[p] * a.c.n_kv_heads + x.h) * kPg;
-#pragma unroll
-          for (int t = 0; t < ATOMS; ++t)
-            tma_load_2d(ring + s * C::kUnitBytes + t * kAtom + p * (kPg * 128), kv ? &tv : &tk, &u_full[s], t * 128,
-                        y, pol);
-        }
-        last[s] = u;
-        return true;
-      };
-      Walker wk = w;
-      wk.skip();
-      w.skip();
-      int gk = 0, gv = 0, jk = 0, jv = 0;
-      bool ok = true;
-      // order of the copies: K0 K1 V0 K2 V1 ..: values are needed a softmax
-      // later than their keys, and would hold a slot meanwhile
-      while (ok && w.valid()) {
-        while (ok && wk.valid() && gk < gv + 2) {
-          ok = load(wk, jk, 0, key_unit(gk));
-          ++gk;
-          if (++jk >= wk.nb) {
-            jk = 0;
-            wk.next();
-            wk.skip();
-          }
-        }
-        ok = ok && load(w, jv, 1, value_unit(gv));
-        ++gv;
-        if (++jv >= w.nb) {
-          jv = 0;
-          w.next();
-          w.skip();
-        }
-      }
-      // every issued copy must land before the CTA may exit
-      for (int i = 0; i < NU; ++i)
-        if (last[i] >= 0) mbar_wait(&u_full[i], (last[i] / NU) & 1, a.c.status);
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      const uint32_t id_qk = idesc_e4m3(kBlk, false), id_pv = idesc_e4m3(D, true);
-      Walker wp = w;
-      w.skip();
-      wp.skip();
-      int js = 0, jp = 0, ip = 0;         // block in item (scores, P V); items begun by P V
-      int nqk = 0, npv = 0, nq = 0;       // blocks issued; query groups begun
-      uint64_t t_last = 0;
-      uint32_t polls = 0;
-      while (wp.valid()) {
-        bool progressed = false;
-        if (npv < nqk) {                  // P V first: it frees a unit
-          const int u = value_unit(npv);
-          bool ready = mbar_test_wait(&p_full[npv & 1], (npv >> 1) & 1) &&
-                       mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
-          if (jp == 0 && ip > 0) ready = ready && mbar_test_wait(o_free, (ip - 1) & 1);
-          if (ready) {
-            tc_fence_after();
-            const uint32_t v_addr = smem_u32(ring + (u % NU) * C::kUnitBytes);
-            const uint32_t p_addr = smem_u32(pbuf + (npv % PB) * kPBytes);
-#pragma unroll
-            for (int kk = 0; kk < kBlk / 32; ++kk)
-              umma_e4m3(tmem, sw128_desc(p_addr + kk * 32), sw128_desc_mn(v_addr + kk * 4096, kAtom), id_pv,
-                        (jp > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&pv_done[npv & 1]);
-            umma_commit(&u_empty[u % NU]);
-            ++npv;
-            if (++jp >= wp.nb) {
-              jp = 0;
-              ++ip;
-              wp.next();
-              wp.skip();
-            }
-            progressed = true;
-          }
-        }
-        if (w.valid()) {
-          const int u = key_unit(nqk);
-          bool ready = mbar_test_wait(&u_full[u % NU], (u / NU) & 1);
-          if (nqk >= SB) ready = ready && mbar_test_wait(&s_free[nqk % SB], ((nqk / SB) - 1) & 1);
-          if (w.fresh) ready = ready && mbar_test_wait(q_ready, nq & 1);
-          if (ready) {
-            if (w.fresh) ++nq;
-            w.fresh = false;
-            tc_fence_after();
-            const uint32_t k_addr = smem_u32(ring + (u % NU) * C::kUnitBytes);
-            const uint32_t t_s = tmem + C::kColS + (nqk % SB) * kBlk;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                umma_e4m3_ta(t_s, tmem + C::kColQ + c * (D / 4) + kk * 8,
-                             sw128_desc(k_addr + (kk >> 2) * kAtom + (kk & 3) * 32), id_qk, (c > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&s_full[nqk % SB]);
-            umma_commit(&u_empty[u % NU]);
-            ++nqk;
-            if (++js >= w.nb) {
-              js = 0;
-              w.next();
-              w.skip();
-            }
-            progressed = true;
-          }
-        }
-        if (progressed) {
-          polls = 0;
-        } else if ((++polls & 1023u) == 0) {
-          const uint64_t now = globaltimer_ns();
-          if (polls == 1024) t_last = now;
-          else if (now - t_last > kWaitNs || *fail) {
-            flag_status(a.c.status, SPEC_DEV_TIMEOUT);
-            *fail = 1;
-            break;
-          }
-        }
-      }
-      // nothing may be in flight when TMEM is freed
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0, a.c.status);
-    }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------- scales
     const int per_page = kPg / a.c.block;
-    int i = 0;
-    for (; w.valid(); w.next()) {
-      if (w.nb == 0) continue;
-      const int h = w.h;
-      if (i >= 2) fwait(&sc_empty[i & 1], ((i >> 1) - 1) & 1, a.c.status, fail);
-      const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
-      const int count = w.nb * (kBlk / a.c.block);
-      for (int e = lane; e < count; e += 32) {
-        const int key = w.blk0 * kBlk + e * a.c.block, pg = key / kPg;
-        float ks = 0.f, vs = -1.f;
-        if (pg * kPg <= w.hi && pg * kPg + kPg - 1 >= w.lo) {
-          const int id = bt[pg];
-          if (id >= 0 && id < a.c.num_pages) {
-            const int64_t sc = (static_cast<int64_t>(id) * a.c.n_kv_heads + h) * per_page + (key % kPg) / a.c.block;
-            ks = a.c.ks[sc];
-            vs = a.c.vs[sc];
+    bool fresh = true;
+    for (int i = 0;; w.next()) {
+      const bool end = !w.valid();
+      const int r0 = w.rb * RP, nrows = end ? 0 : min(a.rows - r0, RP);
+      const long bh = static_cast<long>(w.b) * a.c.n_kv_heads + w.h;
+      const long slot = (bh * a.n_splits + w.sidx) * a.rows + r0;
+      fresh |= w.fresh;
+      w.fresh = false;
+      if (!end && w.nb == 0) {            // no key for this row block in this split
+        for (int r = lane; r < nrows; r += 32) {
+          if (a.n_splits > 1) {
+            __stcg(&a.part_ml[slot + r], make_float2(kNoKey, 0.f));
           } else {
-            flag_status(a.c.status, SPEC_DEV_BAD_PAGE);
+            const long o = (static_cast<long>(w.b) * a.n + (r0 + r) / a.G) * (a.c.n_kv_heads * a.G) + w.h * a.G + (r0 + r) % a.G;
+            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(a.out + o * D + c) = make_uint4(0, 0, 0, 0);
           }
         }
-        ks_s[(i & 1) * kMaxScales + e] = ks;
-        vs_s[(i & 1) * kMaxScales + e] = vs;
+        continue;
+      }
+      const int q = i % kItems;
+      if (i >= kItems) wait(&it_empty[q], ((i / kItems) - 1) & 1);
+      if (lane == 0) {
+        Item& x = items[q];
+        x.h = w.h;
+        x.r0 = r0;
+        x.nrows = nrows;
+        x.p0 = w.L + a.q_offset;
+        x.lo = w.lo;
+        x.hi = w.hi;
+        x.blk0 = w.blk0;
+        x.nb = end ? -1 : w.nb;
+        x.fresh = fresh;
+        x.slot = slot;
+        x.q_row = bh * a.rows + r0;
+        x.page0 = static_cast<long>(w.b) * a.c.max_pages;
+        x.out0 = static_cast<long>(w.b) * a.n;
+      }
+      if (!end) {
+        fresh = false;
+        const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
+        const int count = w.nb * (kBlk / a.c.block);
+        for (int e = lane; e < count; e += 32) {
+          const int key = (w.blk0 << kLgBlk) + e * a.c.block, pg = key / kPg;
+          float ks = 0.f, vs = -1.f;
+          if (pg * kPg <= w.hi && pg * kPg + kPg - 1 >= w.lo) {
+            const int id = bt[pg];
+            if (id >= 0 && id < a.c.num_pages) {
+              const int64_t sc = (static_cast<int64_t>(id) * a.c.n_kv_heads + w.h) * per_page + (key % kPg) / a.c.block;
+              ks = a.c.ks[sc];
+              vs = a.c.vs[sc];
+            } else {
+              flag_status(a.c.status, SPEC_DEV_BAD_PAGE);
+            }
+          }
+          ks_s[q * kMaxScales + e] = ks;
+          vs_s[q * kMaxScales + e] = vs;
+        }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sc_full[i & 1]);
+      if (lane == 0) mbar_arrive(&it_full[q]);
+      if (end || *fail) break;
       ++i;
     }
   } else {
@@ -520,61 +539,64 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     constexpr int kRowThreads = RP == 64 ? 128 : 256;
     const int lg_bt = 31 - __clz(a.c.block);
     float* red_r = red + rh * (NG * 32);
-    int g = 0, item = 0, p = 0;
+    int g = 0, p = 0;
     float qs = 0.f;
-    // To the next item with keys (the partials of those without go out here);
-    // where the queries change, this thread's row of them into TMEM: every
-    // product with the old ones is done once the last scores have been read.
-    auto take = [&]() {
-      for (; w.valid() && w.nb == 0; w.next()) {
-        const int r0 = w.rb * RP;
-        const long slot = ((static_cast<long>(w.b) * a.c.n_kv_heads + w.h) * a.n_splits + w.sidx) * a.rows + r0;
-        if (grp == 0 && row < min(a.rows - r0, RP)) __stcg(&a.part_ml[slot + row], make_float2(kNoKey, 0.f));
-      }
-      if (!w.valid() || !w.fresh) return;
-      w.fresh = false;
-      const int r0 = w.rb * RP;
-      const bool have = row < min(a.rows - r0, RP);
-      const long at = (static_cast<long>(w.b) * a.c.n_kv_heads + w.h) * a.rows + r0 + row;
-      p = w.L + a.q_offset + (r0 + row) / a.G;
+    bool bad_q = false;
+    uint16_t* out_row = nullptr;
+    // Takes item i; where the queries change, this thread's row of them into
+    // TMEM: every product with the old ones is done once the last scores have
+    // been read.  False: there is none.
+    auto take = [&](int i) -> bool {
+      if (!wait(&it_full[i % kItems], (i / kItems) & 1)) return false;
+      const Item& x = items[i % kItems];
+      if (x.nb < 0) return false;
+      if (!x.fresh) return true;
+      const bool have = row < x.nrows;
+      const int r = x.r0 + row, i_pos = r / a.G;
+      p = x.p0 + i_pos;
+      out_row = a.out + ((x.out0 + i_pos) * (a.c.n_kv_heads * a.G) + x.h * a.G + r % a.G) * D;
+      const long at = x.q_row + row, plane = static_cast<long>(a.B) * a.c.n_kv_heads * a.rows;
       qs = have ? a.q_scale[at] : 0.f;
-      qs = qs == qs ? qs * a.scale_log2 : 0.f;        // a NaN row's result is set at the end
-      const long plane = static_cast<long>(a.B) * a.c.n_kv_heads * a.rows;
+      bad_q = qs != qs;                               // a NaN row's result is set at the end
+      qs = bad_q ? 0.f : qs * a.scale_log2;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         const uint4* src = reinterpret_cast<const uint4*>(a.q_codes + (at + c * plane) * D + cg * (D / 2));
         uint32_t v[D / 32][4];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 x = have ? __ldcg(src + i) : make_uint4(0, 0, 0, 0);
-          v[i][0] = x.x;
-          v[i][1] = x.y;
-          v[i][2] = x.z;
-          v[i][3] = x.w;
+        for (int e = 0; e < D / 32; ++e) {
+          const uint4 z = have ? __ldcg(src + e) : make_uint4(0, 0, 0, 0);
+          v[e][0] = z.x;
+          v[e][1] = z.y;
+          v[e][2] = z.z;
+          v[e][3] = z.w;
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          tmem_st8(t_lane + C::kColQ + c * (D / 4) + cg * (D / 8) + i * 8, *reinterpret_cast<uint32_t(*)[8]>(v[2 * i]));
+        for (int e = 0; e < D / 64; ++e)
+          tmem_st8(t_lane + C::kColQ + c * (D / 4) + cg * (D / 8) + e * 8, *reinterpret_cast<uint32_t(*)[8]>(v[2 * e]));
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
+      __syncwarp();
+      return true;
     };
-    take();
-    while (w.valid()) {
-      const int r0 = w.rb * RP, nrows = min(a.rows - r0, RP);
-      const long slot = ((static_cast<long>(w.b) * a.c.n_kv_heads + w.h) * a.n_splits + w.sidx) * a.rows + r0;
+    // (all warps stop together, also after a timeout that only some have seen)
+    bool have_item = take(0);
+    for (int item = 0; !bar_red_or(7, kSoftWarps * 32, !have_item); ++item) {
+      const Item& x = items[item % kItems];
+      const int nrows = x.nrows, x_lo = x.lo, x_hi = x.hi, blk0 = x.blk0, nb = x.nb;
+      const long slot = x.slot;
       const bool half_used = rh * 32 < nrows;         // these warps hold rows
       const bool mine = row < nrows;
-      const int row_lo = max(w.lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(w.hi, p);
-      const float* ks = ks_s + (item & 1) * kMaxScales;
-      const float* vs = vs_s + (item & 1) * kMaxScales;
-      fwait(&sc_full[item & 1], (item >> 1) & 1, a.c.status, fail);
+      const int row_lo = max(x_lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(x_hi, p);
+      const float* ks = ks_s + (item % kItems) * kMaxScales;
+      const float* vs = vs_s + (item % kItems) * kMaxScales;
       float mref = kNoKey, l = 0.f;
-      for (int j = 0; j < w.nb; ++j, ++g) {
-        const int kb = (w.blk0 + j) << kLgBlk, key0 = kb + grp * KW;
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;
         constexpr int NE = KW / 16;                   // scales of the keys (one or two of 16-token blocks)
         float s[KW], f[NE], vsc[NE];
 #pragma unroll
@@ -583,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           vsc[u] = vs[e];
           f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), 3e38f);
         }
-        fwait(&s_full[g % SB], (g / SB) & 1, a.c.status, fail);
+        wait(&s_full[g % SB], (g / SB) & 1);
         __syncwarp();
         tc_fence_after();
         if (half_used) {
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             }
             if (j > 0 && sums && __any_sync(0xffffffffu, al != 1.f)) {
               // the running sums of the moved rows (all earlier P V done)
-              fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
+              wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -677,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           }
         }
         // the P buffer was last read by P V of block g - PB
-        if (g >= PB) fwait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1, a.c.status, fail);
+        if (g >= PB) wait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1);
         if (mine) {
           uint8_t* pp = pbuf + (g % PB) * kPBytes;
 #pragma unroll
@@ -691,9 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         // ---- value rows no row of the item may use: zero them (two threads per key)
         {
           const int key = kb + (st >> 1);
-          if (key < w.lo || key > w.hi || vs[((j << kLgBlk) + (st >> 1)) >> lg_bt] < 0.f) {
+          if (key < x_lo || key > x_hi || vs[((j << kLgBlk) + (st >> 1)) >> lg_bt] < 0.f) {
             const int u = value_unit(g);
-            fwait(&u_full[u % NU], (u / NU) & 1, a.c.status, fail);
+            wait(&u_full[u % NU], (u / NU) & 1);
             uint8_t* vrow = ring + (u % NU) * C::kUnitBytes + (st >> 1) * 128;
 #pragma unroll
             for (int t = 0; t < ATOMS; ++t)
@@ -711,9 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       // o1 / 16) / kUnit: quadrants 0, 1 hold o0 and 2, 3 o1; each finishes half
       // of the columns and passes its sums of the others through shared memory
       // (this row half's part of the P buffer, which no MMA reads now)
-      w.next();
-      take();
-      fwait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.c.status, fail);
+      const bool bad = bad_q;
+      uint16_t* dst = out_row;
+      const int nr = min(32, a.rows - (x.r0 + rh * 32));   // rows of this group of 32
+      have_item = take(item + 1);
+      wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       if (half_used) {
@@ -723,20 +747,20 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < NG; e += 4)
           sum += (red_r[e * 32 + lane] + red_r[e * 32 + 32 + lane]) + (red_r[e * 32 + 64 + lane] + red_r[e * 32 + 96 + lane]);
-        if (grp == 0 && mine && !*fail) __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
+        if (grp == 0 && mine && a.n_splits > 1 && !*fail) __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
         if (sums) {
           constexpr int CW = RP == 32 ? 32 : 16;       // columns a warp finishes at a time
           const bool low = quad >= 2;
           float* give = reinterpret_cast<float*>(pbuf + (64 * cg + 32 * rh) * 128) + (low ? 0 : CW * 32) + lane;
           const float* get = reinterpret_cast<const float*>(pbuf + (64 * cg + 32 * rh) * 128) + (low ? CW * 32 : 0) + lane;
-          float* po = a.part_o + (slot + row) * D;
+          float* po = a.part_o + (slot + rh * 32) * D + lane;
 #pragma unroll 1
           for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 2 * CW) {
-            const int mine0 = c0 + (low ? CW : 0), other0 = c0 + (low ? 0 : CW);
+            const int own0 = c0 + (low ? CW : 0), other0 = c0 + (low ? 0 : CW);
             uint32_t o[CW / 8][8], x[CW / 8][8];
 #pragma unroll
             for (int c = 0; c < CW / 8; ++c) {
-              tmem_ld8_nowait(t_lane + mine0 + 8 * c, o[c]);
+              tmem_ld8_nowait(t_lane + own0 + 8 * c, o[c]);
               tmem_ld8_nowait(t_lane + other0 + 8 * c, x[c]);
             }
             tmem_ld_wait();
@@ -750,9 +774,19 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 #pragma unroll
             for (int c = 0; c < CW; ++c) y[c] = fmaf(y[c], f_get, __uint_as_float(o[c >> 3][c & 7]) * f_own);
             if (mine && !*fail) {
+              if (a.n_splits > 1) {
 #pragma unroll
-              for (int c = 0; c < CW; c += 4)
-                __stcg(reinterpret_cast<float4*>(po + mine0 + c), make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]));
+                for (int c = 0; c < CW; ++c) __stcg(po + (own0 + c) * nr, y[c]);
+              } else {
+                uint32_t h2[CW / 2];
+#pragma unroll
+                for (int c = 0; c < CW; c += 2)
+                  h2[c / 2] = sum == 0.f ? 0u : bad ? 0x7fff7fffu : pack_bf16x2(y[c] / sum, y[c + 1] / sum);
+#pragma unroll
+                for (int c = 0; c < CW; c += 8)
+                  *reinterpret_cast<uint4*>(dst + own0 + c) =
+                      make_uint4(h2[c / 2], h2[c / 2 + 1], h2[c / 2 + 2], h2[c / 2 + 3]);
+              }
             }
             named_bar(bar_cg, 64);
           }
@@ -762,9 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(o_free);
-        mbar_arrive(&sc_empty[item & 1]);
+        mbar_arrive(&it_empty[item % kItems]);
       }
-      ++item;
     }
   }
   tc_fence_before();
@@ -774,62 +807,81 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 }
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row.
-// Four parts by absolute split index mod 4, each in ascending order, then the
-// parts in order: splits without a key of the row add nothing at fixed places,
-// so the order does not depend on where the list of splits starts.  One warp per
-// part, a CTA per row.
-__global__ void __launch_bounds__(128) qattn_combine_kernel(const __grid_constant__ QAttnArgs a) {
-  __shared__ float o_s[4][256];
-  __shared__ float l_s[4], m_s[4];
+// The partials of 32 rows lie [dim][row], as the lanes of the split kernel hold
+// them; a CTA takes 256 such elements next to each other: four parts of 64
+// threads by absolute split index mod 4, each in ascending order, then the parts
+// in order.  Splits without a key of the row add nothing at fixed places, so the
+// order does not depend on where the list of splits starts.
+constexpr int kJoinTile = 32;              // splits whose weights are formed at a time
+__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a) {
+  __shared__ float w_s[kJoinTile][32], l_s[4][32], o_s[4][256];
+  __shared__ float m_s[8][32];
   pdl_trigger();
   pdl_wait();
-  const int r = blockIdx.x % a.rows, bh = blockIdx.x / a.rows;
-  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int D = a.c.dim, i = r / a.G, hq = h * a.G + r % a.G;
-  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + i) * (a.c.n_kv_heads * a.G) + hq) * D;
+  const int groups = (a.rows + 31) / 32, chunks = (a.c.dim * min(a.rows, 32) + 255) / 256;
+  const int bhg = blockIdx.x / chunks, grp = bhg % groups, bh = bhg / groups;
+  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int D = a.c.dim, r0 = grp * 32, nr = min(32, a.rows - r0), e0 = (blockIdx.x % chunks) * 256;
+  if (e0 >= D * nr) return;
   const SeqKeys k = seq_keys(a, a.c.seq_lens[b]);
-  const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r;
+  const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r0;
+  // the rows' largest references
   float M = -INFINITY;
-  for (int s = threadIdx.x; s < k.splits; s += 128) M = fmaxf(M, __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows]).x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (lane == 0) m_s[warp] = M;
+  if (lane < nr)
+    for (int s = warp; s < k.splits; s += 8) M = fmaxf(M, __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + lane]).x);
+  m_s[warp][lane] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
-  float o[8], l = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = 0.f;
-  const int sf = k.splits ? k.lo / a.split : 0, per = D / 32;
-  for (int s = ((warp - sf) & 3); s < k.splits; s += 4) {
-    const float2 ml = __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows]);
-    if (ml.x <= kNoKey) continue;
-    const float wt = exp2f(ml.x - M);
-    const float* po = a.part_o + (slot0 + static_cast<int64_t>(s) * a.rows) * D + lane * per;
-    l = fmaf(wt, ml.y, l);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(po));
-    o[0] = fmaf(wt, x.x, o[0]);
-    o[1] = fmaf(wt, x.y, o[1]);
-    o[2] = fmaf(wt, x.z, o[2]);
-    o[3] = fmaf(wt, x.w, o[3]);
-    if (per == 8) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(po + 4));
-      o[4] = fmaf(wt, y.x, o[4]);
-      o[5] = fmaf(wt, y.y, o[5]);
-      o[6] = fmaf(wt, y.z, o[6]);
-      o[7] = fmaf(wt, y.w, o[7]);
+  for (int v = 0; v < 8; ++v) M = fmaxf(M, m_s[v][lane]);
+  const int part = tid >> 6, t = tid & 63, sf = k.splits ? k.lo / a.split : 0;
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  int row[4];
+  bool in[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int e = e0 + t + 64 * v;
+    in[v] = e < D * nr;
+    row[v] = e % nr;
+  }
+  const float* po = a.part_o + slot0 * D + e0 + t;
+  for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
+    const int ns = min(kJoinTile, k.splits - s0);
+    __syncthreads();
+    // the weight of each split in the tile and, by the same thread, its share of the sum
+    for (int s = warp; s < ns; s += 8) {
+      const float2 ml = lane < nr ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s0 + s) * a.rows + lane])
+                                  : make_float2(kNoKey, 0.f);
+      w_s[s][lane] = ml.x <= kNoKey ? 0.f : exp2f(ml.x - M);
+    }
+    __syncthreads();
+    if (t < nr)
+      for (int s = (part - sf - s0) & 3; s < ns; s += 4)
+        l = fmaf(w_s[s][t], __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s0 + s) * a.rows + t]).y, l);
+#pragma unroll 4
+    for (int s = (part - sf - s0) & 3; s < ns; s += 4) {
+      const float* ps = po + static_cast<int64_t>(s0 + s) * a.rows * D;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float wt = w_s[s][row[v]];
+        // (a split without keys of any row has no sums to read)
+        const float x = in[v] && wt > 0.f ? __ldcg(ps + 64 * v) : 0.f;
+        o[v] = fmaf(wt, x, o[v]);
+      }
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < per) o_s[warp][lane * per + e] = o[e];
-  if (lane == 0) l_s[warp] = l;
   __syncthreads();
-  const float den = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
-  const float qs = a.q_scale[static_cast<int64_t>(bh) * a.rows + r];
-  for (int d = threadIdx.x; d < D; d += 128) {
-    const float x = ((o_s[0][d] + o_s[1][d]) + o_s[2][d]) + o_s[3][d];
-    dst[d] = den == 0.f ? 0 : f32_to_bf16(qs == qs ? x / den : qs);   // no key: zero
-  }
+  if (t < 32) l_s[part][t] = l;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) o_s[part][t + 64 * v] = o[v];
+  __syncthreads();
+  const int e = e0 + tid, d = e / nr, rr = e % nr, q_row = r0 + rr;
+  if (e >= D * nr) return;
+  const float den = (l_s[0][rr] + l_s[1][rr]) + (l_s[2][rr] + l_s[3][rr]);
+  const float x = ((o_s[0][tid] + o_s[1][tid]) + o_s[2][tid]) + o_s[3][tid];
+  const float qs = a.q_scale[static_cast<int64_t>(bh) * a.rows + q_row];
+  const int i = q_row / a.G, hq = h * a.G + q_row % a.G;
+  a.out[((static_cast<int64_t>(b) * a.n + i) * (a.c.n_kv_heads * a.G) + hq) * D + d] =
+      den == 0.f ? 0 : f32_to_bf16(qs == qs ? x / den : qs);   // no key: zero
 }
 
 template <int D, int RP>
@@ -865,7 +917,10 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   const int grid = static_cast<int>(items < sms ? items : sms);
   e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
-  return launch_k(qattn_combine_kernel, dim3(a.B * a.c.n_kv_heads * a.rows), dim3(128), 0, st, a);
+  if (a.n_splits == 1) return cudaSuccess;     // the results are out
+  const int groups = (a.rows + 31) / 32, most = a.rows < 32 ? a.rows : 32;
+  const int64_t ctas = static_cast<int64_t>((D * most + 255) / 256) * a.B * a.c.n_kv_heads * groups;
+  return launch_k(qattn_combine_kernel, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, st, a);
 }
 
 }  // namespace sv

@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(256) qcache_query_kernel(const __grid_constant
   }
   __syncthreads();
   const int per = D / 32, half = r.span / 2;
+  // where results are written by the attention kernel itself, a sequence that
+  // gives it no work gets its zeros here
+  const bool zero = a.n_splits == 1 && seq_keys(a, L).blocks == 0;
   const int64_t plane = static_cast<int64_t>(a.B) * H * a.rows * D;
   for (int hq = warp; hq < H * a.G; hq += 8) {
     const uint16_t* p = a.q + (static_cast<int64_t>(b) * a.n + i) * a.q_row + static_cast<int64_t>(hq) * D;
@@ -169,6 +172,9 @@ __global__ void __launch_bounds__(256) qcache_query_kernel(const __grid_constant
     const int h = hq / a.G, g = hq % a.G;
     const int64_t row = (static_cast<int64_t>(b) * H + h) * a.rows + static_cast<int64_t>(i) * a.G + g;
     uint8_t* dst = a.q_codes + row * D + lane * per;
+    if (zero)
+      for (int e = 0; e < per; ++e)
+        a.out[((static_cast<int64_t>(b) * a.n + i) * H * a.G + hq) * D + lane * per + e] = 0;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       if (e >= per) break;

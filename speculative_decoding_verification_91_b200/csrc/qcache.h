@@ -73,6 +73,22 @@ struct QAttnArgs {
   float2* part_ml;              // [B * Hkv][n_splits][rows] (reference, sum of exponentials)
   uint16_t* out;
 };
+// Keys any row of a sequence may see, as whole blocks; none: blocks = 0.
+constexpr int kQBlk = 128;   // keys of one MMA block
+struct SeqKeys {
+  int lo, hi, splits, blocks;
+};
+__device__ __forceinline__ SeqKeys seq_keys(const QAttnArgs& a, int L) {
+  SeqKeys k{0, -1, 0, 0};
+  if (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * SPEC_PAGE_SIZE) return k;
+  k.hi = min(L + a.kv_extra - 1, L + a.q_offset + a.n - 1);
+  k.lo = a.window > 0 ? max(0, L + a.q_offset - a.window + 1) : 0;
+  if (k.hi < k.lo) return k;
+  k.splits = k.hi / a.split - k.lo / a.split + 1;
+  k.blocks = k.hi / kQBlk - k.lo / kQBlk + 1;
+  return k;
+}
+
 cudaError_t launch_qcache_queries(const RopeArgs& r, const QAttnArgs& a, cudaStream_t st);
 cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st);
 
