@@ -92,8 +92,27 @@ int split_of(const spec_qcache* c) { return c->split_tokens > 0 ? c->split_token
 
 struct AttnLayout {
   size_t codes, scale, part_o, part_ml, total;
-  int n_splits;
+  int split, n_splits;
 };
+
+// Split of a call's attention.  Verify and decode calls (n <= SPEC_MAX_K + 1) take
+// the cache's, so that a row's result depends on neither n nor the batch.  A
+// prompt chunk has row blocks enough to fill the GPU, and a split's partial
+// results cost it more than they give (256 rows over 8k of context, 32 / 4
+// heads: 84 MB of them): it takes the longest split that still leaves four
+// items an SM, up to the kernel's limit of 256 scales.
+constexpr int kItemsWanted = 4 * 148;
+int call_split(const spec_qcache* c, int n_q_heads, int64_t B, int n, int max_pages) {
+  const int split = split_of(c);
+  if (n <= SPEC_MAX_K + 1) return split;
+  const int cap = 256 * c->block_tokens;
+  const int64_t rows = (int64_t)(n_q_heads / c->n_kv_heads) * n;
+  const int64_t groups = B * c->n_kv_heads * ((rows + 63) / 64);
+  const int64_t want = (kItemsWanted + groups - 1) / groups, T = (int64_t)max_pages * SPEC_PAGE_SIZE;
+  int64_t e = ((T + want - 1) / want + kSplitGrain - 1) / kSplitGrain * kSplitGrain;
+  if (e < split) e = split;
+  return (int)(e < cap ? e : cap);
+}
 
 // False where the counts are out of range.
 bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_pages, int window,
@@ -101,12 +120,13 @@ bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_page
   if (n_q_heads < 1 || n_q_heads % c->n_kv_heads || B < 1 || n < 1 || n > SPEC_MAX_PREFILL ||
       max_pages < 1 || max_pages > kMaxPagesPerSeq || window < 0)
     return false;
-  const int64_t splits = ((int64_t)max_pages * SPEC_PAGE_SIZE + split_of(c) - 1) / split_of(c);
+  s->split = call_split(c, n_q_heads, B, n, max_pages);
+  const int64_t splits = ((int64_t)max_pages * SPEC_PAGE_SIZE + s->split - 1) / s->split;
   if (window == 0 && splits > kMaxQSplits) return false;
-  s->n_splits = qcache_splits(max_pages, n, window, split_of(c));
+  s->n_splits = qcache_splits(max_pages, n, window, s->split);
   if (s->n_splits > kMaxQSplits) return false;
   const uint64_t rows = (uint64_t)B * n * n_q_heads;     // (sequence, KV head, row)
-  if (rows > 0x3fffffffull) return false;                // row indices of both codes
+  if (rows > 0x3fffffffull) return false;
   const uint64_t slots = rows * s->n_splits, D = c->head_dim;
   size_t off = kWsHeaderBytes;
   s->codes = off;   off = up256(off + 2 * rows * D);
@@ -115,6 +135,25 @@ bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_page
   s->part_ml = off; off = up256(off + slots * 8);
   s->total = off;
   return true;
+}
+
+// Bytes for any call up to these sizes.  A call of fewer sequences or rows may
+// take a shorter split: with n <= SPEC_MAX_K + 1 the cache's own, beyond that one
+// that leaves at most kItemsWanted + (row blocks) items of 64 rows.
+size_t attn_bytes(const spec_qcache* c, int n_q_heads, int B, int n, int max_pages, int window) {
+  AttnLayout s;
+  if (!attn_layout(c, n_q_heads, B, n, max_pages, window, &s)) return 0;
+  size_t total = s.total;
+  if (n > SPEC_MAX_K + 1) {
+    AttnLayout v;
+    if (!attn_layout(c, n_q_heads, B, SPEC_MAX_K + 1, max_pages, window, &v)) return 0;
+    const uint64_t rows = (uint64_t)B * n * n_q_heads, blocks = rows / 64 + (uint64_t)B * c->n_kv_heads;
+    const uint64_t cap = ((uint64_t)max_pages * SPEC_PAGE_SIZE + 4095) / 4096;
+    const uint64_t slots = 64 * (kItemsWanted + 2 * blocks) + rows * (cap + 1);
+    const size_t most = s.part_o + slots * ((size_t)c->head_dim * 4 + 8) + 512;
+    total = most > v.total ? most : v.total;
+  }
+  return total;
 }
 
 QCacheArgs cache_args(const spec_qcache* c, const int32_t* table, int max_pages, const int32_t* lens,
@@ -203,7 +242,7 @@ int run_attn(const spec_qcache* c, const RopeArgs& r, const AttnCall& k, const A
   a.q_offset = k.q_offset;
   a.kv_extra = k.kv_extra;
   a.window = k.window;
-  a.split = split_of(c);
+  a.split = s.split;
   a.n_splits = s.n_splits;
   a.q = static_cast<const uint16_t*>(k.q);
   a.q_row = k.q_row;
@@ -289,9 +328,8 @@ int spec_qcache_write(const spec_qcache* c, const spec_rope_config* r, const int
 
 size_t spec_qcache_attn_workspace_bytes(const spec_qcache* c, int n_q_heads, int max_batch, int max_n,
                                         int max_pages, int window) {
-  AttnLayout s;
-  if (check_cache(c) || !attn_layout(c, n_q_heads, max_batch, max_n, max_pages, window, &s)) return 0;
-  return s.total;
+  if (check_cache(c)) return 0;
+  return attn_bytes(c, n_q_heads, max_batch, max_n, max_pages, window);
 }
 
 int spec_qcache_attn(const spec_qcache* c, const spec_rope_config* r, const void* q,

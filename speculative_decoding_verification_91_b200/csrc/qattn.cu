@@ -8,8 +8,8 @@
 // brought them, with no conversion of K or V.  The bf16 side of each product is
 // held in two e4m3 codes whose sum keeps 8 bits: queries q = c0 + c1 (from the
 // query kernel; in TMEM; two MMA passes into one accumulator) and weights p = w0 +
-// w1 / 16 (w1 the rounding error of w0, stacked under w0 in the M dimension, so
-// one pass gives both sums, in lanes r and 64 + r of the accumulator).
+// w1 / 16 (w1 the rounding error of w0, other rows of the same M tile, so one
+// pass gives both sums, in lanes 16 apart of the accumulator).
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
@@ -41,6 +41,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "qcache.h"
@@ -59,7 +61,7 @@ constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
 constexpr uint32_t kSmemMax = 227u * 1024u;
 constexpr int kItems = 4;                  // items described ahead in shared memory
 constexpr uint32_t kTail = 12288;
-constexpr uint32_t kPBytes = 128 * kBlk;   // w0 rows 0..63, w1 rows 64..127
+constexpr uint32_t kPBytes = 128 * kBlk;
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
 // p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448.  A larger
 // kLazy moves the reference less often, a larger kUnit keeps smaller weights
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Item* items = reinterpret_cast<Item*>(tail + 512);       // [kItems]
   float* red = reinterpret_cast<float*>(tail + 1024);      // [threads of a row][rows]
+  float* alpha_s = red + 256;                              // [rows]
   float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [kItems][kMaxScales]
   float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -533,16 +536,18 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     const int grp = (RP == 64 ? quad >> 1 : quad) * 2 + cg;       // keys KW grp .. of the block
     const int row = rh * 32 + lane;
     const int st = (warp - kFirstSoft) * 32 + lane;               // 0..255
-    const bool sums = RP == 64 || (quad & 1) == 0;                // lanes that hold sums of w0 (quadrants 0, 1) or w1
+    // Rows of P and of the output: row r in quadrant r / RQ, lane r % RQ for w0,
+    // 16 + r % RQ for w1.  This thread's output row:
+    constexpr int RQ = RP / 4;
+    const int o_idx = lane & 15, o_row = quad * RQ + o_idx;
+    const int p_row = (row / RQ) * 32 + row % RQ;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int bar_rows = 1 + rh, bar_cg = 3 + rh * 2 + cg;
-    constexpr int kRowThreads = RP == 64 ? 128 : 256;
+    constexpr int kSoft = kSoftWarps * 32;
     const int lg_bt = 31 - __clz(a.c.block);
-    float* red_r = red + rh * (NG * 32);
+    float* red_r = red + rh * 32;              // [thread of the row][RP rows]
     int g = 0, p = 0;
     float qs = 0.f;
     bool bad_q = false;
-    uint16_t* out_row = nullptr;
     // Takes item i; where the queries change, this thread's row of them into
     // TMEM: every product with the old ones is done once the last scores have
     // been read.  False: there is none.
@@ -554,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const bool have = row < x.nrows;
       const int r = x.r0 + row, i_pos = r / a.G;
       p = x.p0 + i_pos;
-      out_row = a.out + ((x.out0 + i_pos) * (a.c.n_kv_heads * a.G) + x.h * a.G + r % a.G) * D;
       const long at = x.q_row + row, plane = static_cast<long>(a.B) * a.c.n_kv_heads * a.rows;
       qs = have ? a.q_scale[at] : 0.f;
       bad_q = qs != qs;                               // a NaN row's result is set at the end
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     };
     // (all warps stop together, also after a timeout that only some have seen)
     bool have_item = take(0);
-    for (int item = 0; !bar_red_or(7, kSoftWarps * 32, !have_item); ++item) {
+    for (int item = 0; !bar_red_or(2, kSoft, !have_item); ++item) {
       const Item& x = items[item % kItems];
       const int nrows = x.nrows, x_lo = x.lo, x_hi = x.hi, blk0 = x.blk0, nb = x.nb;
       const long slot = x.slot;
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       for (int j = 0; j < nb; ++j, ++g) {
         const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;
         constexpr int NE = KW / 16;                   // scales of the keys (one or two of 16-token blocks)
-        float s[KW], f[NE], vsc[NE];
+        float s[KW], f[NE], vsc[NE], cand = -INFINITY;
 #pragma unroll
         for (int u = 0; u < NE; ++u) {
           const int e = ((j << kLgBlk) + grp * KW + 16 * u) >> lg_bt;
@@ -626,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             for (int c = 0; c < KW; ++c)
               if (key0 + c < row_lo || key0 + c > row_hi || vsc[c >> 4] < 0.f) s[c] = -INFINITY;
           }
-          float cand = -INFINITY;
 #pragma unroll
           for (int u = 0; u < NE; ++u) {
             float m4[4];
@@ -640,23 +643,27 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             cand = fmaxf(cand, fmaf(mx, f[u], static_cast<float>(lv)));
           }
           __syncwarp();
-          if (bar_red_or(bar_rows, kRowThreads, mine && cand > mref + kLazy)) {
-            red_r[grp * 32 + lane] = cand;
-            named_bar(bar_rows, kRowThreads);
-            float bm = red_r[lane];
+        }
+        if (bar_red_or(1, kSoft, mine && cand > mref + kLazy)) {
+          red_r[grp * RP + lane] = cand;
+          named_bar(1, kSoft);
+          float bm = red_r[lane];
 #pragma unroll
-            for (int e = 1; e < NG; ++e) bm = fmaxf(bm, red_r[e * 32 + lane]);
-            float al = 1.f;
-            if (mine && bm > mref + kLazy) {
-              al = ex2(mref - bm);            // 0 while the row had no key
-              mref = bm;
-              l *= al;
-            }
-            if (j > 0 && sums && __any_sync(0xffffffffu, al != 1.f)) {
-              // the running sums of the moved rows (all earlier P V done)
-              wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-              __syncwarp();
-              tc_fence_after();
+          for (int e = 1; e < NG; ++e) bm = fmaxf(bm, red_r[e * RP + lane]);
+          float al = 1.f;
+          if (mine && bm > mref + kLazy) {
+            al = ex2(mref - bm);              // 0 while the row had no key
+            mref = bm;
+            l *= al;
+          }
+          if (j > 0) {
+            // the running sums of the rows that moved (all earlier P V done)
+            if (grp == 0) alpha_s[row] = al;
+            wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+            named_bar(1, kSoft);
+            tc_fence_after();
+            al = o_row < nrows && o_idx < RQ ? alpha_s[o_row] : 1.f;
+            if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 1
               for (int c = cg * (D / 2); c < (cg + 1) * (D / 2); c += 32) {
                 uint32_t r8[4][8];
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                  for (int x = 0; x < 8; ++x) r8[e][x] = __float_as_uint(__uint_as_float(r8[e][x]) * al);
+                  for (int z = 0; z < 8; ++z) r8[e][z] = __float_as_uint(__uint_as_float(r8[e][z]) * al);
                   tmem_st8(t_lane + c + 8 * e, r8[e]);
                 }
               }
@@ -704,9 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           uint8_t* pp = pbuf + (g % PB) * kPBytes;
 #pragma unroll
           for (int u = 0; u < NE; ++u) {
-            *reinterpret_cast<uint4*>(pp + swz128(row, NE * grp + u)) =
+            *reinterpret_cast<uint4*>(pp + swz128(p_row, NE * grp + u)) =
                 make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
-            *reinterpret_cast<uint4*>(pp + swz128(64 + row, NE * grp + u)) =
+            *reinterpret_cast<uint4*>(pp + swz128(p_row + 16, NE * grp + u)) =
                 make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
           }
         }
@@ -729,67 +736,67 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
-      // ---- on to the next item's queries, then this one's (m, l) and o = (o0 +
-      // o1 / 16) / kUnit: quadrants 0, 1 hold o0 and 2, 3 o1; each finishes half
-      // of the columns and passes its sums of the others through shared memory
-      // (this row half's part of the P buffer, which no MMA reads now)
+      // ---- this item's l, the next item's queries, then (m, l) and o = (o0 + o1
+      // / 16) / kUnit, lanes 16 apart adding two columns at a time
+      const int nr = min(RQ, nrows - quad * RQ);      // output rows of this quadrant
+      float* po = a.part_o + (slot + quad * RQ) * D + o_idx;
+      const long out_at = a.n_splits == 1 ? x.out0 + (x.r0 + o_row) / a.G : 0;
+      const int out_h = a.n_splits == 1 ? x.h * a.G + (x.r0 + o_row) % a.G : 0;
       const bool bad = bad_q;
-      uint16_t* dst = out_row;
-      const int nr = min(32, a.rows - (x.r0 + rh * 32));   // rows of this group of 32
       have_item = take(item + 1);
       wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-      __syncwarp();
+      // (every warp is past the last block's reductions)
+      red_r[grp * RP + lane] = l;
+      if (grp == 0) alpha_s[row] = bad ? 1.f : 0.f;
+      named_bar(1, kSoft);
       tc_fence_after();
-      if (half_used) {
-        red_r[grp * 32 + lane] = l;           // every warp is past the last block's reductions
-        named_bar(bar_rows, kRowThreads);
+      if (grp == 0 && mine && a.n_splits > 1 && !*fail) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < NG; e += 4)
-          sum += (red_r[e * 32 + lane] + red_r[e * 32 + 32 + lane]) + (red_r[e * 32 + 64 + lane] + red_r[e * 32 + 96 + lane]);
-        if (grp == 0 && mine && a.n_splits > 1 && !*fail) __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
-        if (sums) {
-          constexpr int CW = RP == 32 ? 32 : 16;       // columns a warp finishes at a time
-          const bool low = quad >= 2;
-          float* give = reinterpret_cast<float*>(pbuf + (64 * cg + 32 * rh) * 128) + (low ? 0 : CW * 32) + lane;
-          const float* get = reinterpret_cast<const float*>(pbuf + (64 * cg + 32 * rh) * 128) + (low ? CW * 32 : 0) + lane;
-          float* po = a.part_o + (slot + rh * 32) * D + lane;
+        for (int e = 0; e < NG; ++e) sum += red_r[e * RP + lane];
+        __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
+      }
+      if (nr > 0) {
+        const bool low = lane >= 16, store = o_idx < nr && !*fail;
+        const float f_own = low ? 1.f / (kUnit * kLow) : 1.f / kUnit, f_got = low ? 1.f / kUnit : 1.f / (kUnit * kLow);
+        float sum = 0.f;
+        uint16_t* dst = nullptr;
+        if (a.n_splits == 1 && store) {
+          dst = a.out + (out_at * (a.c.n_kv_heads * a.G) + out_h) * D;
+#pragma unroll
+          for (int e = 0; e < NG; ++e) sum += red[e * RP + o_row];
+          if (alpha_s[o_row] != 0.f) sum = __int_as_float(0x7fffffff);    // a NaN query
+        }
+        // the lanes of w0's sums finish the columns at 0, step, .. and those of w1's
+        // the ones at off, off + step, .. of 32
+        auto finish = [&](auto step_, auto off_, auto&& out) {
+          constexpr int step = decltype(step_)::value, off = decltype(off_)::value;
 #pragma unroll 1
-          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 2 * CW) {
-            const int own0 = c0 + (low ? CW : 0), other0 = c0 + (low ? 0 : CW);
-            uint32_t o[CW / 8][8], x[CW / 8][8];
+          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 32) {
+            float o[32], y[16];
+            tmem_ld32(t_lane + c0, o);
 #pragma unroll
-            for (int c = 0; c < CW / 8; ++c) {
-              tmem_ld8_nowait(t_lane + own0 + 8 * c, o[c]);
-              tmem_ld8_nowait(t_lane + other0 + 8 * c, x[c]);
+            for (int c = 0; c < 16; ++c) {
+              const float got = __shfl_xor_sync(0xffffffffu, low ? o[step * c] : o[step * c + off], 16);
+              y[c] = fmaf(got, f_got, (low ? o[step * c + off] : o[step * c]) * f_own);
             }
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < CW; ++c) give[c * 32] = __uint_as_float(x[c >> 3][c & 7]);
-            named_bar(bar_cg, 64);
-            float y[CW];
-            const float f_own = low ? 1.f / (kUnit * kLow) : 1.f / kUnit, f_get = low ? 1.f / kUnit : 1.f / (kUnit * kLow);
-#pragma unroll
-            for (int c = 0; c < CW; ++c) y[c] = get[c * 32];
-#pragma unroll
-            for (int c = 0; c < CW; ++c) y[c] = fmaf(y[c], f_get, __uint_as_float(o[c >> 3][c & 7]) * f_own);
-            if (mine && !*fail) {
-              if (a.n_splits > 1) {
-#pragma unroll
-                for (int c = 0; c < CW; ++c) __stcg(po + (own0 + c) * nr, y[c]);
-              } else {
-                uint32_t h2[CW / 2];
-#pragma unroll
-                for (int c = 0; c < CW; c += 2)
-                  h2[c / 2] = sum == 0.f ? 0u : bad ? 0x7fff7fffu : pack_bf16x2(y[c] / sum, y[c + 1] / sum);
-#pragma unroll
-                for (int c = 0; c < CW; c += 8)
-                  *reinterpret_cast<uint4*>(dst + own0 + c) =
-                      make_uint4(h2[c / 2], h2[c / 2 + 1], h2[c / 2 + 2], h2[c / 2 + 3]);
-              }
-            }
-            named_bar(bar_cg, 64);
+            if (store) out(c0 + (low ? off : 0), y);
           }
+        };
+        if (a.n_splits > 1) {     // [dim][row]: two whole dims a store
+          finish(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{}, [&](int c0, const float(&y)[16]) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) __stcg(po + (c0 + 2 * c) * nr, y[c]);
+          });
+        } else {                  // the row's result: 16 dims next to each other
+          finish(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{}, [&](int c0, const float(&y)[16]) {
+            uint32_t v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = sum == 0.f ? 0u : pack_bf16x2(y[2 * c] / sum, y[2 * c + 1] / sum);
+            uint4* d = reinterpret_cast<uint4*>(dst + c0);
+            d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          });
         }
       }
       tc_fence_before();
@@ -807,81 +814,105 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 }
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row.
-// The partials of 32 rows lie [dim][row], as the lanes of the split kernel hold
-// them; a CTA takes 256 such elements next to each other: four parts of 64
-// threads by absolute split index mod 4, each in ascending order, then the parts
-// in order.  Splits without a key of the row add nothing at fixed places, so the
-// order does not depend on where the list of splits starts.
-constexpr int kJoinTile = 32;              // splits whose weights are formed at a time
-__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a) {
-  __shared__ float w_s[kJoinTile][32], l_s[4][32], o_s[4][256];
-  __shared__ float m_s[8][32];
+// The partials of the rq rows of a group (a lane quadrant of the split kernel)
+// lie [dim][row].  A CTA takes a group and, x of gridDim.x / groups, every xs-th
+// run of whole dims of about 256 elements: four parts of 64 threads by absolute
+// split index mod 4, each in ascending order, then the parts in order.  Splits
+// without a key of the row add nothing at fixed places, so the order does not
+// depend on where the list of splits starts.  References and sums of up to
+// kJoinTile splits come in one round of loads, and four splits' partials are in
+// flight at a time: with a load at a time this took 50 us for 128 splits.
+constexpr int kJoinTile = 128;
+__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a, int rq, int xs) {
+  __shared__ float w_s[kJoinTile][16], l_s[kJoinTile][16];
+  __shared__ float o_s[4][256], den_s[4][16], m_s[16][16];
   pdl_trigger();
   pdl_wait();
-  const int groups = (a.rows + 31) / 32, chunks = (a.c.dim * min(a.rows, 32) + 255) / 256;
-  const int bhg = blockIdx.x / chunks, grp = bhg % groups, bh = bhg / groups;
-  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int D = a.c.dim, r0 = grp * 32, nr = min(32, a.rows - r0), e0 = (blockIdx.x % chunks) * 256;
-  if (e0 >= D * nr) return;
+  const int groups = (a.rows + rq - 1) / rq, x = blockIdx.x % xs, bhg = blockIdx.x / xs;
+  const int grp = bhg % groups, bh = bhg / groups;
+  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads, tid = threadIdx.x;
+  const int D = a.c.dim, r0 = grp * rq, nr = min(rq, a.rows - r0);
   const SeqKeys k = seq_keys(a, a.c.seq_lens[b]);
+  const int sf = k.splits ? k.lo / a.split : 0;
   const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r0;
-  // the rows' largest references
-  float M = -INFINITY;
-  if (lane < nr)
-    for (int s = warp; s < k.splits; s += 8) M = fmaxf(M, __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + lane]).x);
-  m_s[warp][lane] = M;
+  const int tr = tid & 15, ts = tid >> 4;          // row, split (of 16 at a time)
+  const int part = tid >> 6, t = tid & 63;
+  auto load_tile = [&](int s0) {                   // references into w_s, sums into l_s
+#pragma unroll
+    for (int i = 0; i < kJoinTile / 16; ++i) {
+      const int s = s0 + i * 16 + ts;
+      float2 ml = make_float2(kNoKey, 0.f);
+      if (tr < nr && s < k.splits) ml = __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + tr]);
+      w_s[i * 16 + ts][tr] = ml.x;
+      l_s[i * 16 + ts][tr] = ml.y;
+    }
+  };
+  float M = kNoKey;
+  for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
+    load_tile(s0);                                 // each thread reads back what it wrote
+#pragma unroll
+    for (int i = 0; i < kJoinTile / 16; ++i) M = fmaxf(M, w_s[i * 16 + ts][tr]);
+  }
+  m_s[ts][tr] = M;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < 8; ++v) M = fmaxf(M, m_s[v][lane]);
-  const int part = tid >> 6, t = tid & 63, sf = k.splits ? k.lo / a.split : 0;
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  int row[4];
-  bool in[4];
+  for (int i = 0; i < 16; ++i) M = fmaxf(M, m_s[i][tr]);
+  const bool once = k.splits <= kJoinTile;
+  int cols = 256 / nr;                             // whole dims of a run: a power of two
+  cols = min(1 << (31 - __clz(cols)), D);
+  const int lg = 31 - __clz(cols), run = cols * nr;
+  float den = 0.f;
+  for (int c0 = x * cols; c0 < D; c0 += xs * cols) {
+    const bool first = c0 == x * cols;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    int row[4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int e = e0 + t + 64 * v;
-    in[v] = e < D * nr;
-    row[v] = e % nr;
-  }
-  const float* po = a.part_o + slot0 * D + e0 + t;
-  for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
-    const int ns = min(kJoinTile, k.splits - s0);
-    __syncthreads();
-    // the weight of each split in the tile and, by the same thread, its share of the sum
-    for (int s = warp; s < ns; s += 8) {
-      const float2 ml = lane < nr ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s0 + s) * a.rows + lane])
-                                  : make_float2(kNoKey, 0.f);
-      w_s[s][lane] = ml.x <= kNoKey ? 0.f : exp2f(ml.x - M);
-    }
-    __syncthreads();
-    if (t < nr)
-      for (int s = (part - sf - s0) & 3; s < ns; s += 4)
-        l = fmaf(w_s[s][t], __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s0 + s) * a.rows + t]).y, l);
+    for (int v = 0; v < 4; ++v) row[v] = (t + 64 * v) % nr;
+    for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
+      const int ns = min(kJoinTile, k.splits - s0);
+      if (!once || first) {
+        if (!once) {
+          __syncthreads();
+          load_tile(s0);
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinTile / 16; ++i) {
+          const float m = w_s[i * 16 + ts][tr];
+          w_s[i * 16 + ts][tr] = m <= kNoKey ? 0.f : exp2f(m - M);
+        }
+        __syncthreads();
+        if (first && t < 16)
+          for (int s = (part - sf - s0) & 3; s < ns; s += 4) den = fmaf(w_s[s][t], l_s[s][t], den);
+      }
+      const float* po = a.part_o + slot0 * D + static_cast<int64_t>(s0) * a.rows * D + static_cast<int64_t>(c0) * nr + t;
 #pragma unroll 4
-    for (int s = (part - sf - s0) & 3; s < ns; s += 4) {
-      const float* ps = po + static_cast<int64_t>(s0 + s) * a.rows * D;
+      for (int s = (part - sf - s0) & 3; s < ns; s += 4) {
+        const float* ps = po + static_cast<int64_t>(s) * a.rows * D;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float wt = w_s[s][row[v]];
-        // (a split without keys of any row has no sums to read)
-        const float x = in[v] && wt > 0.f ? __ldcg(ps + 64 * v) : 0.f;
-        o[v] = fmaf(wt, x, o[v]);
+        for (int v = 0; v < 4; ++v) {
+          const float wt = w_s[s][row[v]];
+          // (a split without keys of the row has no sums to read)
+          const float z = t + 64 * v < run && wt > 0.f ? __ldcg(ps + 64 * v) : 0.f;
+          o[v] = fmaf(wt, z, o[v]);
+        }
       }
     }
-  }
-  __syncthreads();
-  if (t < 32) l_s[part][t] = l;
+    if (first && t < 16) den_s[part][t] = den;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) o_s[part][t + 64 * v] = o[v];
-  __syncthreads();
-  const int e = e0 + tid, d = e / nr, rr = e % nr, q_row = r0 + rr;
-  if (e >= D * nr) return;
-  const float den = (l_s[0][rr] + l_s[1][rr]) + (l_s[2][rr] + l_s[3][rr]);
-  const float x = ((o_s[0][tid] + o_s[1][tid]) + o_s[2][tid]) + o_s[3][tid];
-  const float qs = a.q_scale[static_cast<int64_t>(bh) * a.rows + q_row];
-  const int i = q_row / a.G, hq = h * a.G + q_row % a.G;
-  a.out[((static_cast<int64_t>(b) * a.n + i) * (a.c.n_kv_heads * a.G) + hq) * D + d] =
-      den == 0.f ? 0 : f32_to_bf16(qs == qs ? x / den : qs);   // no key: zero
+    for (int v = 0; v < 4; ++v) o_s[part][t + 64 * v] = o[v];
+    __syncthreads();
+    // a thread per result, a row's dims next to each other
+    if (tid < run) {
+      const int r = tid >> lg, c = tid & (cols - 1), e = c * nr + r, q_row = r0 + r;
+      const float l = (den_s[0][r] + den_s[1][r]) + (den_s[2][r] + den_s[3][r]);
+      const float y = ((o_s[0][e] + o_s[1][e]) + o_s[2][e]) + o_s[3][e];
+      const float qs = a.q_scale[static_cast<int64_t>(bh) * a.rows + q_row];
+      const int i = q_row / a.G, hq = h * a.G + q_row % a.G;
+      a.out[((static_cast<int64_t>(b) * a.n + i) * (a.c.n_kv_heads * a.G) + hq) * D + c0 + c] =
+          l == 0.f ? 0 : f32_to_bf16(qs == qs ? y / l : qs);   // no key: zero
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, int RP>
@@ -918,9 +949,14 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   if (a.n_splits == 1) return cudaSuccess;     // the results are out
-  const int groups = (a.rows + 31) / 32, most = a.rows < 32 ? a.rows : 32;
-  const int64_t ctas = static_cast<int64_t>((D * most + 255) / 256) * a.B * a.c.n_kv_heads * groups;
-  return launch_k(qattn_combine_kernel, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, st, a);
+  // (sequence, KV head, row group) by runs of dims: about four CTAs an SM
+  const int rq = rp / 4, nr = a.rows < rq ? a.rows : rq;
+  const int64_t groups = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rq - 1) / rq);
+  int cols = 1;
+  while (2 * cols * nr <= 256 && 2 * cols <= D) cols *= 2;
+  const int64_t runs = D / cols, want = (4 * sms + groups - 1) / groups;
+  const int xs = static_cast<int>(runs < want ? runs : want);
+  return launch_k(qattn_combine_kernel, dim3(static_cast<unsigned>(groups * xs)), dim3(256), 0, st, a, rq, xs);
 }
 
 }  // namespace sv
