@@ -814,104 +814,123 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 }
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row.
-// The partials of the rq rows of a group (a lane quadrant of the split kernel)
-// lie [dim][row].  A CTA takes a group and, x of gridDim.x / groups, every xs-th
-// run of whole dims of about 256 elements: four parts of 64 threads by absolute
-// split index mod 4, each in ascending order, then the parts in order.  Splits
-// without a key of the row add nothing at fixed places, so the order does not
-// depend on where the list of splits starts.  References and sums of up to
-// kJoinTile splits come in one round of loads, and four splits' partials are in
-// flight at a time: with a load at a time this took 50 us for 128 splits.
-constexpr int kJoinTile = 128;
-__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a, int rq, int xs) {
-  __shared__ float w_s[kJoinTile][16], l_s[kJoinTile][16];
-  __shared__ float o_s[4][256], den_s[4][16], m_s[16][16];
+// The partials of the rq <= 16 rows of a group (a lane quadrant of the split
+// kernel) lie [dim][row].  A CTA takes 16 V dims of a group, a thread V of them of
+// one row; it keeps four sums by split index mod 4, each in ascending order, and
+// adds them in the order of the absolute index.  Splits without a key of the row
+// add nothing at fixed places, so the order does not depend on where the list of
+// splits starts, and V and U change nothing.  The time is a chain of memory
+// latencies: the sequence's length, the references and the first U splits'
+// partials are all asked for at once, those beyond the sequence's last split
+// (whatever the workspace holds) are dropped.
+constexpr int kJoinTile = 128;             // splits whose weights are held at a time
+template <int V, int U>
+__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a, int rq) {
+  __shared__ float w_s[kJoinTile][16], l_s[kJoinTile][16], m_s[16][16];
+  __shared__ float y_s[16][16 * V + 1];
   pdl_trigger();
   pdl_wait();
-  const int groups = (a.rows + rq - 1) / rq, x = blockIdx.x % xs, bhg = blockIdx.x / xs;
-  const int grp = bhg % groups, bh = bhg / groups;
-  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads, tid = threadIdx.x;
-  const int D = a.c.dim, r0 = grp * rq, nr = min(rq, a.rows - r0);
-  const SeqKeys k = seq_keys(a, a.c.seq_lens[b]);
-  const int sf = k.splits ? k.lo / a.split : 0;
+  const int D = a.c.dim, runs = D / (16 * V), groups = (a.rows + rq - 1) / rq;
+  const int run = blockIdx.x % runs, bhg = blockIdx.x / runs, grp = bhg % groups, bh = bhg / groups;
+  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads;
+  const int row = threadIdx.x & 15, tc = threadIdx.x >> 4;
+  const int r0 = grp * rq, nr = min(rq, a.rows - r0);
   const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r0;
-  const int tr = tid & 15, ts = tid >> 4;          // row, split (of 16 at a time)
-  const int part = tid >> 6, t = tid & 63;
+  const int L = a.c.seq_lens[b];
+  const bool mine = row < nr;
+  const float qs = mine ? a.q_scale[static_cast<int64_t>(bh) * a.rows + r0 + row] : 0.f;
+  const float* po = a.part_o + slot0 * D + static_cast<int64_t>(run * 16 * V + tc) * nr + row;
+  const int64_t step = static_cast<int64_t>(a.rows) * D;
+  float x[U][V];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        x[u][v] = mine && s0 + u < a.n_splits ? __ldcg(po + (s0 + u) * step + 16 * v * nr) : 0.f;
+  };
   auto load_tile = [&](int s0) {                   // references into w_s, sums into l_s
+    float2 ml[kJoinTile / 16];
 #pragma unroll
     for (int i = 0; i < kJoinTile / 16; ++i) {
-      const int s = s0 + i * 16 + ts;
-      float2 ml = make_float2(kNoKey, 0.f);
-      if (tr < nr && s < k.splits) ml = __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + tr]);
-      w_s[i * 16 + ts][tr] = ml.x;
-      l_s[i * 16 + ts][tr] = ml.y;
+      const int s = s0 + i * 16 + tc;
+      ml[i] = mine && s < a.n_splits ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + row])
+                                     : make_float2(kNoKey, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinTile / 16; ++i) {
+      w_s[i * 16 + tc][row] = ml[i].x;
+      l_s[i * 16 + tc][row] = ml[i].y;
     }
   };
+  load(0);
+  load_tile(0);
+  const SeqKeys k = seq_keys(a, L);
   float M = kNoKey;
   for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
-    load_tile(s0);                                 // each thread reads back what it wrote
-#pragma unroll
-    for (int i = 0; i < kJoinTile / 16; ++i) M = fmaxf(M, w_s[i * 16 + ts][tr]);
+    if (s0 > 0) load_tile(s0);                     // each thread reads back what it wrote
+    for (int s = tc; s < min(kJoinTile, k.splits - s0); s += 16) M = fmaxf(M, w_s[s][row]);
   }
-  m_s[ts][tr] = M;
+  m_s[tc][row] = M;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) M = fmaxf(M, m_s[i][tr]);
-  const bool once = k.splits <= kJoinTile;
-  int cols = 256 / nr;                             // whole dims of a run: a power of two
-  cols = min(1 << (31 - __clz(cols)), D);
-  const int lg = 31 - __clz(cols), run = cols * nr;
-  float den = 0.f;
-  for (int c0 = x * cols; c0 < D; c0 += xs * cols) {
-    const bool first = c0 == x * cols;
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    int row[4];
+  for (int i = 0; i < 16; ++i) M = fmaxf(M, m_s[i][row]);
+  float acc[4][V], den[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < 4; ++v) row[v] = (t + 64 * v) % nr;
-    for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
-      const int ns = min(kJoinTile, k.splits - s0);
-      if (!once || first) {
-        if (!once) {
-          __syncthreads();
-          load_tile(s0);
-        }
+  for (int p = 0; p < 4; ++p)
 #pragma unroll
-        for (int i = 0; i < kJoinTile / 16; ++i) {
-          const float m = w_s[i * 16 + ts][tr];
-          w_s[i * 16 + ts][tr] = m <= kNoKey ? 0.f : exp2f(m - M);
-        }
-        __syncthreads();
-        if (first && t < 16)
-          for (int s = (part - sf - s0) & 3; s < ns; s += 4) den = fmaf(w_s[s][t], l_s[s][t], den);
-      }
-      const float* po = a.part_o + slot0 * D + static_cast<int64_t>(s0) * a.rows * D + static_cast<int64_t>(c0) * nr + t;
-#pragma unroll 4
-      for (int s = (part - sf - s0) & 3; s < ns; s += 4) {
-        const float* ps = po + static_cast<int64_t>(s) * a.rows * D;
+    for (int v = 0; v < V; ++v) acc[p][v] = 0.f;
+  for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
+    const int ns = min(kJoinTile, k.splits - s0);
+    if (k.splits > kJoinTile) {
+      __syncthreads();
+      load_tile(s0);
+    }
+    for (int s = tc; s < ns; s += 16) {
+      const float m = w_s[s][row];
+      w_s[s][row] = m <= kNoKey ? 0.f : exp2f(m - M);
+    }
+    __syncthreads();
+    for (int u0 = 0; u0 < ns; u0 += U) {
+      if (s0 + u0 > 0) load(s0 + u0);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float wt = w_s[s][row[v]];
-          // (a split without keys of the row has no sums to read)
-          const float z = t + 64 * v < run && wt > 0.f ? __ldcg(ps + 64 * v) : 0.f;
-          o[v] = fmaf(wt, z, o[v]);
+      for (int u = 0; u < U; ++u) {
+        const float w = u0 + u < ns ? w_s[u0 + u][row] : 0.f;
+        if (w > 0.f) {                             // (a split without keys of the row has no sums)
+          den[u & 3] = fmaf(w, l_s[u0 + u][row], den[u & 3]);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[u & 3][v] = fmaf(w, x[u][v], acc[u & 3][v]);
         }
       }
     }
-    if (first && t < 16) den_s[part][t] = den;
+  }
+  // the four sums in the order of the absolute split index
+  const int turn = k.splits ? (k.lo / a.split) & 3 : 0;
+  auto ordered = [&](const float(&q)[4]) {
+    float z[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) o_s[part][t + 64 * v] = o[v];
-    __syncthreads();
-    // a thread per result, a row's dims next to each other
-    if (tid < run) {
-      const int r = tid >> lg, c = tid & (cols - 1), e = c * nr + r, q_row = r0 + r;
-      const float l = (den_s[0][r] + den_s[1][r]) + (den_s[2][r] + den_s[3][r]);
-      const float y = ((o_s[0][e] + o_s[1][e]) + o_s[2][e]) + o_s[3][e];
-      const float qs = a.q_scale[static_cast<int64_t>(bh) * a.rows + q_row];
-      const int i = q_row / a.G, hq = h * a.G + q_row % a.G;
-      a.out[((static_cast<int64_t>(b) * a.n + i) * (a.c.n_kv_heads * a.G) + hq) * D + c0 + c] =
-          l == 0.f ? 0 : f32_to_bf16(qs == qs ? y / l : qs);   // no key: zero
-    }
-    __syncthreads();
+    for (int p = 0; p < 4; ++p)
+      z[p] = turn == 0 ? q[p] : turn == 1 ? q[(p + 3) & 3] : turn == 2 ? q[(p + 2) & 3] : q[(p + 1) & 3];
+    return ((z[0] + z[1]) + z[2]) + z[3];
+  };
+  const float l = ordered(den);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float q[4] = {acc[0][v], acc[1][v], acc[2][v], acc[3][v]};
+    const float y = ordered(q);
+    y_s[row][tc + 16 * v] = l == 0.f ? 0.f : qs == qs ? y / l : qs;   // no key: zero
+  }
+  __syncthreads();
+  const int orow = threadIdx.x >> 4, q_row = r0 + orow, c = (threadIdx.x & 15) * V;
+  if (orow >= nr) return;
+  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + q_row / a.G) * (a.c.n_kv_heads * a.G) + h * a.G + q_row % a.G) * D +
+                  run * 16 * V + c;
+  if (V == 1) {
+    dst[0] = f32_to_bf16(y_s[orow][c]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<uint32_t*>(dst + v) = pack_bf16x2(y_s[orow][c + v], y_s[orow][c + v + 1]);
   }
 }
 
@@ -949,14 +968,13 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   if (a.n_splits == 1) return cudaSuccess;     // the results are out
-  // (sequence, KV head, row group) by runs of dims: about four CTAs an SM
-  const int rq = rp / 4, nr = a.rows < rq ? a.rows : rq;
+  // long lists of splits: fewer dims and more splits in flight in a thread (128
+  // splits of 36 rows: TUNED)
+  const int rq = rp / 4;
   const int64_t groups = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rq - 1) / rq);
-  int cols = 1;
-  while (2 * cols * nr <= 256 && 2 * cols <= D) cols *= 2;
-  const int64_t runs = D / cols, want = (4 * sms + groups - 1) / groups;
-  const int xs = static_cast<int>(runs < want ? runs : want);
-  return launch_k(qattn_combine_kernel, dim3(static_cast<unsigned>(groups * xs)), dim3(256), 0, st, a, rq, xs);
+  if (a.n_splits > 40)
+    return launch_k(qattn_combine_kernel<1, 32>, dim3(static_cast<unsigned>(groups * (D / 16))), dim3(256), 0, st, a, rq);
+  return launch_k(qattn_combine_kernel<4, 8>, dim3(static_cast<unsigned>(groups * (D / 64))), dim3(256), 0, st, a, rq);
 }
 
 }  // namespace sv

@@ -119,49 +119,65 @@ __global__ void __launch_bounds__(kWriteThreads) qcache_write_kernel(const __gri
 // hold a query to 2^-9 of itself (and 2^-19 of the row's largest), finer than
 // bf16's 2^-9 on average, and both factors of the score product are e4m3.  A
 // row with an infinity or NaN gets a NaN scale, which makes its result NaN.
-__global__ void __launch_bounds__(256) qcache_query_kernel(const __grid_constant__ RopeArgs r,
+// A CTA takes a row of a sequence and every blockIdx.y-th four of its heads, a warp a head (4 or
+// 8 dims a lane): the row's angles once for all of them (each warp forming its own took 41 us
+// instead of TUNED for 512 rows of 32 heads), the first head asked for before.
+template <int D>
+__global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant__ RopeArgs r,
                                                            const __grid_constant__ QAttnArgs a) {
+  constexpr int P = D / 32;
   __shared__ float2 cs[kMaxPairs];
   pdl_trigger();
   pdl_wait();
-  const int i = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int D = a.c.dim, H = a.c.n_kv_heads;
+  const int H = a.c.n_kv_heads, n_heads = H * a.G, lane = threadIdx.x & 31;
+  const int64_t bi = blockIdx.x;
+  const int b = static_cast<int>(bi / a.n), i = static_cast<int>(bi % a.n);
   const int L = a.c.seq_lens[b];
-  const int pos = min(max(L, 0), 1 << 30) + a.q_offset + i;
-  for (int j = threadIdx.x; j < r.n_rot; j += 256) {
-    double c, s;
-    rope_turn(pos, r.turns[j], c, s);
-    cs[j] = make_float2(static_cast<float>(c * r.magnitude), static_cast<float>(s * r.magnitude));
+  const int half = r.span / 2;
+  int pair[P], partner[P];   // pair of the dim, -1: passes through; the second of its pair: + kMaxPairs
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    const int d = lane * P + e;
+    int j = -1, w = d;
+    if (r.layout == SPEC_ROPE_HALF) {
+      if (d < r.n_rot) j = d, w = d + half;
+      else if (d >= half && d < half + r.n_rot) j = d - half + kMaxPairs, w = d - half;
+    } else if (d < 2 * r.n_rot) {
+      j = (d >> 1) + (d & 1) * kMaxPairs;
+      w = d ^ 1;
+    }
+    pair[e] = j;
+    partner[e] = w;
+  }
+  float own[P], with[P];
+  auto load = [&](int hq) {
+    const uint16_t* p = a.q + bi * a.q_row + static_cast<int64_t>(hq) * D;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      own[e] = bf16_to_f32(p[lane * P + e]);
+      with[e] = bf16_to_f32(p[partner[e]]);
+    }
+  };
+  int hq = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (hq < n_heads) load(hq);
+  if (threadIdx.x < r.n_rot) {
+    const int pos = min(max(L, 0), 1 << 30) + a.q_offset + i;
+    float c, s;
+    rope_turn(pos, r.turns[threadIdx.x], static_cast<float>(r.magnitude), c, s);
+    cs[threadIdx.x] = make_float2(c, s);
   }
   __syncthreads();
-  const int per = D / 32, half = r.span / 2;
-  // where results are written by the attention kernel itself, a sequence that
-  // gives it no work gets its zeros here
-  const bool zero = a.n_splits == 1 && seq_keys(a, L).blocks == 0;
-  const int64_t plane = static_cast<int64_t>(a.B) * H * a.rows * D;
-  for (int hq = warp; hq < H * a.G; hq += 8) {
-    const uint16_t* p = a.q + (static_cast<int64_t>(b) * a.n + i) * a.q_row + static_cast<int64_t>(hq) * D;
-    float y[8], amax = 0.f;
+  for (; hq < n_heads; hq += gridDim.y * 4) {
+    if (hq >= static_cast<int>(gridDim.y) * 4) load(hq);
+    float amax = 0.f;
     bool bad = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (e >= per) break;
-      const int d = lane * per + e;
-      int j = -1, w = d;
-      bool second = false;
-      if (r.layout == SPEC_ROPE_HALF) {
-        if (d < r.n_rot) j = d, w = d + half;
-        else if (d >= half && d < half + r.n_rot) j = d - half, w = j, second = true;
-      } else if (d < 2 * r.n_rot) {
-        j = d >> 1, w = d ^ 1, second = d & 1;
+    for (int e = 0; e < P; ++e) {
+      if (pair[e] >= 0) {
+        const float2 t = cs[pair[e] & (kMaxPairs - 1)];
+        own[e] = pair[e] >= kMaxPairs ? with[e] * t.y + own[e] * t.x : own[e] * t.x - with[e] * t.y;
       }
-      float x = bf16_to_f32(p[d]);
-      if (j >= 0) {
-        const float x2 = bf16_to_f32(p[w]);
-        x = second ? x2 * cs[j].y + x * cs[j].x : x * cs[j].x - x2 * cs[j].y;
-      }
-      y[e] = x;
-      if (finite_f(x)) amax = fmaxf(amax, fabsf(x));
+      if (finite_f(own[e])) amax = fmaxf(amax, fabsf(own[e]));
       else bad = true;
     }
 #pragma unroll
@@ -171,20 +187,31 @@ __global__ void __launch_bounds__(256) qcache_query_kernel(const __grid_constant
     const float inv = pow2f(-e2);
     const int h = hq / a.G, g = hq % a.G;
     const int64_t row = (static_cast<int64_t>(b) * H + h) * a.rows + static_cast<int64_t>(i) * a.G + g;
-    uint8_t* dst = a.q_codes + row * D + lane * per;
-    if (zero)
-      for (int e = 0; e < per; ++e)
-        a.out[((static_cast<int64_t>(b) * a.n + i) * H * a.G + hq) * D + lane * per + e] = 0;
+    const int64_t plane = static_cast<int64_t>(a.B) * H * a.rows * D;
+    uint32_t c0[P / 4], c1[P / 4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      if (e >= per) break;
-      const float u = bad ? 0.f : y[e] * inv, v = bad ? 0.f : y[e + 1] * inv;
-      const uint32_t c0 = e4m3x2(u, v);
-      const float2 f = e4m3_values(c0);
-      *reinterpret_cast<uint16_t*>(dst + e) = c0;
-      *reinterpret_cast<uint16_t*>(dst + plane + e) = e4m3x2(u - f.x, v - f.y);
+    for (int e = 0; e < P; e += 2) {
+      const float u = bad ? 0.f : own[e] * inv, v = bad ? 0.f : own[e + 1] * inv;
+      const uint32_t x = e4m3x2(u, v);
+      const float2 f = e4m3_values(x);
+      const uint32_t y = e4m3x2(u - f.x, v - f.y);
+      c0[e / 4] = e % 4 ? c0[e / 4] | x << 16 : x;
+      c1[e / 4] = e % 4 ? c1[e / 4] | y << 16 : y;
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.q_codes + row * D + lane * P);
+    uint32_t* dst1 = reinterpret_cast<uint32_t*>(a.q_codes + plane + row * D + lane * P);
+#pragma unroll
+    for (int e = 0; e < P / 4; ++e) {
+      dst[e] = c0[e];
+      dst1[e] = c1[e];
     }
     if (lane == 0) a.q_scale[row] = bad ? __int_as_float(0x7fffffff) : pow2f(e2);
+    // where results are written by the attention kernel itself, a sequence that
+    // gives it no work gets its zeros here
+    if (a.n_splits == 1 && seq_keys(a, L).blocks == 0) {
+#pragma unroll
+      for (int e = 0; e < P; e += 2) *reinterpret_cast<uint32_t*>(a.out + (bi * n_heads + hq) * D + lane * P + e) = 0u;
+    }
   }
 }
 
@@ -201,7 +228,11 @@ cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStre
 }
 
 cudaError_t launch_qcache_queries(const RopeArgs& r, const QAttnArgs& a, cudaStream_t st) {
-  return launch_k(qcache_query_kernel, dim3(a.n, a.B), dim3(256), 0, st, r, a);
+  // few rows: a warp for every head; many: the angles of a row formed once
+  const int n_heads = a.c.n_kv_heads * a.G, rows = a.B * a.n;
+  const dim3 grid(rows, rows >= 148 ? 1 : (n_heads + 3) / 4);
+  return a.c.dim == 256 ? launch_k(qcache_query_kernel<256>, grid, dim3(128), 0, st, r, a)
+                        : launch_k(qcache_query_kernel<128>, grid, dim3(128), 0, st, r, a);
 }
 
 int qcache_splits(int max_pages, int n, int window, int split) {

@@ -27,6 +27,19 @@ __device__ __forceinline__ void rope_turn(int pos, double turns, double& c, doub
   sincospi(2.0 * (t - rint(t)), &s, &c);
 }
 
+// magnitude * (cos, sin) in binary32: the turn's fraction is reduced in binary64
+// and split into a binary32 head and tail; the tail enters to first order, so
+// the results are off by little more than half a step.
+__device__ __forceinline__ void rope_turn(int pos, double turns, float magnitude, float& c, float& s) {
+  const double t = static_cast<double>(pos) * turns;
+  const double f = t - rint(t);
+  const float hi = static_cast<float>(f), lo = static_cast<float>(f - hi) * 6.2831853f;
+  float sh, ch;
+  sincospif(2.f * hi, &sh, &ch);
+  c = (ch - sh * lo) * magnitude;
+  s = (sh + ch * lo) * magnitude;
+}
+
 // ---------------------------------------------------------------- spec_rope
 struct RopeOpArgs {
   const void* x;
