@@ -938,8 +938,8 @@ template <int D, int RP>
 cudaError_t launch_one(int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                        const QAttnArgs& a, cudaStream_t st) {
   auto kern = qattn_kernel<D, RP>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kern, Cfg<D>::kSmem, allowed);
   if (e != cudaSuccess) return e;
   return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, tk, tv, a);
 }

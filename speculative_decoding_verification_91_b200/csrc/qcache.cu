@@ -2,6 +2,8 @@
 // queries' form for the attention over it (qattn.cu).
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "qcache.h"
@@ -12,6 +14,8 @@ namespace {
 
 constexpr int kPg = SPEC_PAGE_SIZE;
 constexpr int kWriteThreads = 256;
+constexpr int kWriteWarps = kWriteThreads / 32;
+constexpr int kWriteList = 1024;        // entries formed again in binary64 at the end of a CTA
 
 __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) <= 3.4028234e38f; }
 
@@ -24,7 +28,8 @@ __device__ __forceinline__ float to_odd(double y) {
 }
 
 // Element d of a head of the row at p, turned by r at pos, rounded to odd.
-__device__ __forceinline__ float turned(const RopeArgs& r, const uint16_t* p, int d, int pos) {
+// (Out of line: needed for a few entries in 10^4.)
+__device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d, int pos) {
   const int half = r.span / 2;
   int j = -1, e = d;          // pair and partner dim
   bool second = false;
@@ -44,74 +49,264 @@ __device__ __forceinline__ float turned(const RopeArgs& r, const uint16_t* p, in
   return to_odd(second ? w * s + x * c : x * c - w * s);
 }
 
-// One CTA per (touched block of tokens, KV head, sequence), keys (z even) or
-// values (z odd).
-__global__ void __launch_bounds__(kWriteThreads) qcache_write_kernel(const __grid_constant__ RopeArgs r,
-                                                                     const __grid_constant__ QWriteArgs a) {
-  extern __shared__ float rows[];            // [block][dim]
-  __shared__ float red[kWriteThreads / 32];
+// The append.  A CTA takes one touched block of BT tokens of a sequence, keys (the
+// first half of z) or values, for `heads` KV heads one after the other: its 8 warps
+// hold the block's new rows in registers (a lane 8 dims, IT rows of each warp), find
+// the largest magnitude, settle the scale and store the codes, the next head's rows
+// on their way meanwhile; every row is read once.  The angles of the block's rows are
+// formed once, in shared memory.  Bound by instruction issue and latency: TUNED
+//
+// Codes are those of the exactly turned key.  Keys turn in binary32, off by less
+// than kTurnErr (|x0| + |x1|) magnitude: cosine and sine 1.5 steps and a rounding by
+// the magnitude each, the product, the sum, 4.5 x 2^-24.  Where rounding that much
+// lower and higher (by a lane's largest own and partner's magnitude) gives two codes
+// (3 in 10^4) the entry is formed again in binary64, all of a CTA's together at its
+// end.  Blocks with infinities or NaN, blocks whose scale would turn on that error,
+// and half pairs whose distance is no multiple of 8 take binary64 throughout.  (All
+// of it in binary64, with each head its own angles, took 545 us for 64 x 256 tokens
+// of 8 heads; entries formed again where they were found, 160-230; a warp a head that
+// reads its rows twice, 135.)
+constexpr float kTurnErr = 4.6f / 16777216.f;
+
+__device__ __forceinline__ __nv_bfloat162 abs2(uint32_t w) {
+  w &= 0x7fff7fffu;
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+// max that hands a NaN on
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+template <int D, int BT>
+__global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __grid_constant__ RopeArgs r,
+                                                                        const __grid_constant__ QWriteArgs a, int heads,
+                                                                        int n_tab) {
+  constexpr int LR = D / 8;                  // lanes of a row
+  constexpr int RI = 32 / LR;                // rows of a warp at a time
+  constexpr int IT = BT / (kWriteWarps * RI) > 0 ? BT / (kWriteWarps * RI) : 1;
+  extern __shared__ float2 cs[];             // [BT][n_tab], (1, 0) past the turned pairs; 8 times (1, 0)
+  __shared__ uint32_t red[2][kWriteWarps];
+  __shared__ int list_n;
+  __shared__ int2 list[kWriteList];          // (head of the CTA, row, dim), the scale's inverse
   pdl_trigger();
   pdl_wait();
   const QCacheArgs& c = a.c;
-  const int b = blockIdx.z >> 1, is_v = blockIdx.z & 1, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // keys first: their CTAs take longer
+  const int is_v = blockIdx.z >= gridDim.z / 2, b = blockIdx.z - (is_v ? gridDim.z / 2 : 0);
   const int L = c.seq_lens[b];
   if (L < 0 || static_cast<int64_t>(L) + a.n > static_cast<int64_t>(c.max_pages) * kPg) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0) flag_status(c.status, SPEC_DEV_BAD_LENGTH);
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) flag_status(c.status, SPEC_DEV_BAD_LENGTH);
     return;
   }
-  const int p0 = (L / c.block + static_cast<int>(blockIdx.x)) * c.block;   // first position of the block
+  const int p0 = (L / BT + static_cast<int>(blockIdx.x)) * BT;   // first position of the block
   if (p0 >= L + a.n) return;
   const int page = c.block_table[static_cast<int64_t>(b) * c.max_pages + p0 / kPg];
   if (page < 0 || page >= c.num_pages) {
     if (threadIdx.x == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
     return;
   }
-  const int lo = max(p0, L), hi = min(p0 + c.block, L + a.n);   // new positions
-  const int D = c.dim;
-  const uint16_t* src = is_v ? a.v_new : a.k_new;
+  const int lo = max(p0, L) - p0, hi = min(BT, L + a.n - p0);    // new rows of the block
+  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, c.n_kv_heads);
   const int64_t stride = is_v ? a.v_row : a.k_row;
-  float amax = 0.f;
-  bool bad = false;
-  for (int i = threadIdx.x; i < (hi - lo) * D; i += kWriteThreads) {
-    const int pos = lo + i / D, d = i % D;
-    const uint16_t* p = src + (static_cast<int64_t>(b) * a.n + (pos - L)) * stride + static_cast<int64_t>(h) * D;
-    const float y = is_v ? bf16_to_f32(p[d]) : turned(r, p, d, pos);
-    rows[i] = y;
-    if (finite_f(y)) amax = fmaxf(amax, fabsf(y));
-    else bad = true;
-  }
-  if (bad) flag_status(c.status, SPEC_DEV_NONFINITE);
+  const int d0 = (lane % LR) * 8, t0 = warp * IT * RI + lane / LR;   // dims; rows t0, t0 + RI, ..
+  const uint16_t* block0 = (is_v ? a.v_new : a.k_new) + (static_cast<int64_t>(b) * a.n + (p0 - L)) * stride;   // row 0
+  uint32_t there = 0;                        // bit i: row t0 + i RI is new
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  for (int w = 0; w < kWriteThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-
-  const int64_t head = static_cast<int64_t>(page) * c.n_kv_heads + h;
-  float* sc = (is_v ? c.vs : c.ks) + head * (kPg / c.block) + (p0 % kPg) / c.block;
-  uint8_t* dst = (is_v ? c.v : c.k) + (head * kPg + p0 % kPg) * D;
-  float now = pow2f(scale_exponent(amax));
-  const float was = *sc;
-  if (lo > p0) {
-    now = fmaxf(now, was);
-    if (now > was) {                         // rewrite the committed codes for the larger scale
-      const float ratio = __fdiv_rn(was, now);
-      for (int i = threadIdx.x; i < (lo - p0) * D / 2; i += kWriteThreads) {
-        uint16_t* q = reinterpret_cast<uint16_t*>(dst) + i;
-        const float2 v = e4m3_values(*q);
-        *q = e4m3x2(v.x == v.x ? v.x * ratio : 0.f, v.y == v.y ? v.y * ratio : 0.f);
+  for (int i = 0; i < IT; ++i) there |= (t0 + i * RI >= lo && t0 + i * RI < hi) ? 1u << i : 0u;
+  uint4 raw[IT];
+  auto load = [&](int h) {
+    const uint16_t* p = block0 + t0 * stride + h * D + d0;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+      raw[i] = there >> i & 1 ? __ldg(reinterpret_cast<const uint4*>(p + i * RI * stride)) : make_uint4(0, 0, 0, 0);
+  };
+  load(h0);
+  if (threadIdx.x == 0) list_n = 0;
+  const bool half = r.layout == SPEC_ROPE_HALF, turns_keys = !is_v && r.n_rot > 0;
+  const int hs = r.span / 2;
+  float2* none = cs + BT * n_tab;
+  if (turns_keys) {
+    const int j = threadIdx.x % n_tab, step = kWriteThreads / n_tab;   // a thread's pair stays, its row advances
+    const double turn = j < r.n_rot ? r.turns[j] : 0.0;
+    if (threadIdx.x < 8) none[threadIdx.x] = make_float2(1.f, 0.f);
+    for (int t = lo + threadIdx.x / n_tab; t < hi && threadIdx.x < step * n_tab; t += step) {
+      float ca = 1.f, sa = 0.f;
+      if (j < r.n_rot) rope_turn(p0 + t, turn, static_cast<float>(r.magnitude), ca, sa);
+      cs[t * n_tab + j] = make_float2(ca, sa);
+    }
+  }
+  // this lane's dims: pairs from j0 on (-1: they pass through); for half pairs the
+  // partners lie `from` lanes away
+  int j0 = -1, from = lane;
+  uint32_t flip = 0x80008000u;               // signs of the partners' products
+  if (turns_keys) {
+    if (!half) {
+      if (d0 / 2 < r.n_rot) j0 = d0 / 2;
+    } else if (hs % 8 == 0 && d0 < r.span) {
+      const bool second = d0 >= hs;
+      const int j = second ? d0 - hs : d0;
+      if (j < r.n_rot) {
+        j0 = j;
+        from = lane + (second ? -hs / 8 : hs / 8);
+        if (second) flip = 0;
       }
     }
   }
-  const float inv = __fdiv_rn(1.f, now);
-  for (int i = threadIdx.x; i < (hi - lo) * D / 2; i += kWriteThreads) {
-    float v[2] = {rows[2 * i], rows[2 * i + 1]};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) v[e] = v[e] == v[e] ? v[e] * inv : 0.f;
-    reinterpret_cast<uint16_t*>(dst + (lo - p0) * D)[i] = e4m3x2(v[0], v[1]);
-  }
+  const bool plain = !(turns_keys && half && hs % 8 != 0);
   __syncthreads();
-  if (threadIdx.x == 0) *sc = now;
+  auto block_max = [&](float x, int buf) {   // as bits (NaN above all)
+    uint32_t m = __float_as_uint(x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane == 0) red[buf][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kWriteWarps; ++v) m = max(m, red[buf][v]);
+    return m;
+  };
+
+  for (int h = h0; h < h1; ++h) {
+    float y[IT][8], amax = 0.f, err = 0.f;
+    __nv_bfloat162 top = abs2(0u), with = top;   // largest own and partner's magnitudes
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[i][2 * e] = __uint_as_float(w[e] << 16);
+        y[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+      if (turns_keys) {
+        // (dims that pass through turn by (1, 0), half pairs with themselves)
+        const float4* ct = reinterpret_cast<const float4*>(j0 >= 0 && (there >> i & 1) ? cs + (t0 + i * RI) * n_tab + j0 : none);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __hmax2(top, abs2(w[e]));
+        if (half) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t o = __shfl_sync(0xffffffffu, w[e], from) ^ flip;
+            const float4 q = ct[e];
+            with = __hmax2(with, abs2(o));
+            y[i][2 * e] = fmaf(__uint_as_float(o << 16), q.y, y[i][2 * e] * q.x);
+            y[i][2 * e + 1] = fmaf(__uint_as_float(o & 0xffff0000u), q.w, y[i][2 * e + 1] * q.z);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 q = ct[e];
+            const float x0 = y[i][4 * e], x1 = y[i][4 * e + 1], x2 = y[i][4 * e + 2], x3 = y[i][4 * e + 3];
+            y[i][4 * e] = x0 * q.x - x1 * q.y;
+            y[i][4 * e + 1] = x0 * q.y + x1 * q.x;
+            y[i][4 * e + 2] = x2 * q.z - x3 * q.w;
+            y[i][4 * e + 3] = x2 * q.w + x3 * q.z;
+          }
+        }
+      }
+      float m[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[e] = max_nan(fabsf(y[i][2 * e]), fabsf(y[i][2 * e + 1]));
+      amax = max_nan(amax, max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])));
+    }
+    if (h + 1 < h1) load(h + 1);
+    if (j0 >= 0) {
+      if (!half) with = top;
+      err = kTurnErr * static_cast<float>(r.magnitude) *
+            (fmaxf(__low2float(top), __high2float(top)) + fmaxf(__low2float(with), __high2float(with)));
+    }
+    uint32_t m = block_max(plain ? amax : INFINITY, h & 1);
+    // the scale turns at 1.75 x 2^x: a turned magnitude is within 2 kTurnErr,
+    // 8 steps of binary32, of it
+    const bool exact = m >= 0x7f800000u || (turns_keys && abs(static_cast<int>(m & 0x7fffffu) - 0x600000) <= 16);
+    const uint16_t* head0 = block0 + h * D;
+    // the entries one by one, in binary64
+    auto entries = [&](auto&& f) {
+#pragma unroll 1
+      for (int i = 0; i < IT; ++i) {
+        if (!(there >> i & 1)) continue;
+        const int t = t0 + i * RI;
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e)
+          f(t, e, is_v ? bf16_to_f32(head0[t * stride + d0 + e]) : turned(r, head0 + t * stride, d0 + e, p0 + t));
+      }
+    };
+    if (exact) {                             // (uniform in the CTA)
+      bool bad = false;
+      amax = 0.f;
+      entries([&](int, int, float v) {
+        if (finite_f(v)) amax = fmaxf(amax, fabsf(v));
+        else bad = true;
+      });
+      if (bad) flag_status(c.status, SPEC_DEV_NONFINITE);
+      __syncthreads();
+      m = block_max(amax, h & 1);
+    }
+    amax = __uint_as_float(m);
+    const int64_t head = static_cast<int64_t>(page) * c.n_kv_heads + h;
+    float* sc = (is_v ? c.vs : c.ks) + head * (kPg / BT) + (p0 % kPg) / BT;
+    uint8_t* dst = (is_v ? c.v : c.k) + (head * kPg + p0 % kPg) * D;
+    const int e2 = scale_exponent(amax);
+    float now = pow2f(e2), inv = pow2f(-e2);
+    if (lo > 0) {                              // committed tokens share the block
+      const float was = *sc;
+      now = fmaxf(now, was);
+      if (now == was) inv = __fdiv_rn(1.f, was);
+      if (now > was) {                         // rewrite their codes for the larger scale
+        const float ratio = __fdiv_rn(was, now);
+        for (int i = threadIdx.x; i < lo * D / 2; i += kWriteThreads) {
+          uint16_t* q = reinterpret_cast<uint16_t*>(dst) + i;
+          const float2 v = e4m3_values(*q);
+          *q = e4m3x2(v.x == v.x ? v.x * ratio : 0.f, v.y == v.y ? v.y * ratio : 0.f);
+        }
+      }
+    }
+    if (exact) {
+      entries([&](int t, int e, float v) {
+        dst[t * D + d0 + e] = static_cast<uint8_t>(e4m3x2(v == v ? v * inv : 0.f, 0.f));
+      });
+    } else {
+      err *= inv;                              // (0 where nothing turns, and for rows of zeros)
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        auto codes = [&](float add) {
+          uint32_t q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = e4m3x2(fmaf(y[i][2 * e], inv, add), fmaf(y[i][2 * e + 1], inv, add));
+          return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+        };
+        const uint2 code = codes(-err);
+        if (!(there >> i & 1)) continue;
+        *reinterpret_cast<uint2*>(dst + (t0 + i * RI) * D + d0) = code;
+        if (is_v) continue;
+        const uint2 up = codes(err);
+        uint32_t dx = code.x ^ up.x, dy = code.y ^ up.y;
+        while (dx | dy) {
+          const int e = (__ffs(dx ? dx : dy) - 1) >> 3, at = atomicAdd(&list_n, 1);
+          if (at < kWriteList)
+            list[at] = make_int2((h - h0) << 16 | (t0 + i * RI) << 8 | (d0 + e + (dx ? 0 : 4)), __float_as_int(inv));
+          if (dx) dx &= ~(0xffu << (8 * e));
+          else dy &= ~(0xffu << (8 * e));
+        }
+      }
+    }
+    __syncthreads();                           // everyone has read the old scale
+    if (threadIdx.x == 0) *sc = now;
+  }
+  // ---- the entries next to a rounding border, over what was stored above (every one
+  // of the CTA's, should they be more than the list holds)
+  __syncthreads();
+  const bool all = list_n > kWriteList;
+  const int n = all ? (h1 - h0) * (hi - lo) * D : list_n;
+  for (int i = threadIdx.x; i < n; i += kWriteThreads) {
+    const int h = h0 + (all ? i / D / (hi - lo) : static_cast<uint32_t>(list[i].x) >> 16);
+    const int t = all ? lo + i / D % (hi - lo) : list[i].x >> 8 & 0xff, d = all ? i % D : list[i].x & 0xff;
+    const int64_t head = static_cast<int64_t>(page) * c.n_kv_heads + h;
+    const float inv = all ? __fdiv_rn(1.f, c.ks[head * (kPg / BT) + (p0 % kPg) / BT]) : __int_as_float(list[i].y);
+    const float v = turned(r, block0 + t * stride + h * D, d, p0 + t);
+    c.k[(head * kPg + p0 % kPg + t) * D + d] = static_cast<uint8_t>(e4m3x2(v == v ? v * inv : 0.f, 0.f));
+  }
 }
 
 // Queries: one warp per head of a row.  q = q_scale * (code0 + code1): the
@@ -217,14 +412,31 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
 
 }  // namespace
 
-cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st) {
-  const int blocks = (a.n + a.c.block - 2) / a.c.block + 1;   // that n tokens may touch
-  const size_t smem = static_cast<size_t>(a.c.block) * a.c.dim * 4;
-  cudaError_t e = cudaFuncSetAttribute(qcache_write_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       64 * 256 * 4);
+template <int D, int BT>
+cudaError_t launch_write(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st) {
+  const int blocks = (a.n + BT - 2) / BT + 1;                    // that n tokens may touch
+  // one head a CTA until the GPU is full, then as many as share its angles
+  const int64_t per_head = 2ll * blocks * a.B;
+  const int heads = static_cast<int>(std::min<int64_t>(a.c.n_kv_heads, std::max<int64_t>(1, per_head * a.c.n_kv_heads / (8 * 148))));
+  const int n_tab = (r.n_rot + 7) / 8 * 8;
+  const size_t smem = (static_cast<size_t>(BT) * n_tab + 8) * sizeof(float2);
+  auto kern = qcache_write_kernel<D, BT>;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kern, (BT * kMaxPairs + 8) * static_cast<int>(sizeof(float2)), allowed);
   if (e != cudaSuccess) return e;
-  return launch_k(qcache_write_kernel, dim3(blocks, a.c.n_kv_heads, 2 * a.B), dim3(kWriteThreads), smem, st,
-                  r, a);
+  return launch_k(kern, dim3(blocks, (a.c.n_kv_heads + heads - 1) / heads, 2 * a.B), dim3(kWriteThreads), smem, st,
+                  r, a, heads, n_tab);
+}
+
+template <int D>
+cudaError_t launch_write_dim(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st) {
+  return a.c.block == 64   ? launch_write<D, 64>(r, a, st)
+         : a.c.block == 32 ? launch_write<D, 32>(r, a, st)
+                           : launch_write<D, 16>(r, a, st);
+}
+
+cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStream_t st) {
+  return a.c.dim == 256 ? launch_write_dim<256>(r, a, st) : launch_write_dim<128>(r, a, st);
 }
 
 cudaError_t launch_qcache_queries(const RopeArgs& r, const QAttnArgs& a, cudaStream_t st) {

@@ -6,11 +6,27 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace sv {
 
 constexpr int kMaxPairs = SPEC_ROPE_MAX_DIM / 2;
+
+// Raises a kernel's limit of dynamic shared memory, once per device (the driver
+// call costs a microsecond or more of every launch otherwise).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (f == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return f;
+}
 
 // A rotary configuration as the kernels take it: turns[j] = f_j / (2 pi), so
 // the angle's reduction is exact (a subtraction of a whole number).

@@ -1,6 +1,22 @@
 // Rotary positions on strided rows of heads (spec_rope): half or interleaved
 // pairs over part of the head, any frequencies, forwards or back.
+//
+//   y0 = x0 c - x1 s,  y1 = x0 s + x1 c,   (c, s) = magnitude (cos, sin)(t f_j)
+//
+// Bound by memory: every element is read and written once.  A CTA takes `rows`
+// rows of `heads` heads; their cosines and sines are formed once in shared
+// memory, while the first loads are on their way (a thread's own angles for every
+// pair would be 30 instructions an element).  Two forms:
+//   direct  where 16-byte pieces hold whole pairs (interleaved) or lie opposite
+//           each other (half: span / 2 a multiple of the piece): a thread turns a
+//           piece, or two opposite ones, in registers.
+//   staged  any other span or alignment: the heads pass through shared memory, in
+//           16-byte pieces where rows and heads are aligned to them, else element
+//           by element.
+// 32,768 rows of 8 x 256 bf16, interleaved: TUNED
 #include <math.h>
+
+#include <algorithm>
 
 #include <cuda_fp16.h>
 
@@ -13,69 +29,208 @@ namespace sv {
 namespace {
 
 constexpr int kRopeOpThreads = 256;
+constexpr int kRopeRows = 32;           // rows of a CTA
+constexpr int kRopeTile = 16384;        // bytes of heads of a CTA
+
+// i / d for i, d < 65536: mul = floor(2^32 / d) + 1 (d = 1: handled apart)
+struct Div {
+  uint32_t d, mul;
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1 ? i : __umulhi(i, mul); }
+};
+Div make_div(int d) { return Div{static_cast<uint32_t>(d), static_cast<uint32_t>((1ull << 32) / d) + 1}; }
+
+struct RopePlan {
+  int rows, heads, head_blocks;   // of a CTA; CTAs across the heads
+  int units;                      // pieces (direct) of a head
+  Div by_units, by_heads, by_pairs;
+};
 
 template <typename T>
-__device__ __forceinline__ float rope_load(const T* p);
+__device__ __forceinline__ float to_f(T v);
 template <>
-__device__ __forceinline__ float rope_load<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float to_f<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
 template <>
-__device__ __forceinline__ float rope_load<__half>(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
 template <>
-__device__ __forceinline__ float rope_load<float>(const float* p) { return *p; }
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
 template <typename T>
-__device__ __forceinline__ void rope_store(T* p, float v);
+__device__ __forceinline__ T from_f(float v);
 template <>
-__device__ __forceinline__ void rope_store<uint16_t>(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+__device__ __forceinline__ uint16_t from_f<uint16_t>(float v) { return f32_to_bf16(v); }
 template <>
-__device__ __forceinline__ void rope_store<__half>(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 template <>
-__device__ __forceinline__ void rope_store<float>(float* p, float v) { *p = v; }
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
 
-// One CTA per row: the row's cosines and sines once, then a thread per pair of
-// any head, then the dims that pass through (nothing to do in place).
 template <typename T>
-__global__ void __launch_bounds__(kRopeOpThreads) rope_kernel(const __grid_constant__ RopeArgs r,
-                                                              const __grid_constant__ RopeOpArgs a) {
-  __shared__ float2 cs[kMaxPairs];
-  pdl_trigger();
-  pdl_wait();
-  const int64_t row = blockIdx.x;
-  const int pos = a.positions[row];
-  if (pos < 0) return;
-  for (int j = threadIdx.x; j < r.n_rot; j += kRopeOpThreads) {
-    double c, s;
-    rope_turn(pos, r.turns[j], c, s);
-    cs[j] = make_float2(static_cast<float>(c * r.magnitude),
-                        static_cast<float>(s * (a.inverse ? -r.magnitude : r.magnitude)));
+union Piece {
+  uint4 v;
+  T e[16 / sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ void turn(T& a, T& b, float2 cs) {
+  const float x0 = to_f<T>(a), x1 = to_f<T>(b);
+  a = from_f<T>(x0 * cs.x - x1 * cs.y);
+  b = from_f<T>(x0 * cs.y + x1 * cs.x);
+}
+
+// Positions and (c, s) of the CTA's rows; ends with a barrier.
+__device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, const RopePlan& p, int64_t row0,
+                                       float2* cs, int* pos) {
+  const int n = p.rows * r.n_rot;
+  if (threadIdx.x < p.rows)
+    pos[threadIdx.x] = row0 + threadIdx.x < a.n_rows ? a.positions[row0 + threadIdx.x] : -1;
+  for (int i = threadIdx.x; i < n; i += kRopeOpThreads) {
+    const int t = p.by_pairs(i), j = i - t * r.n_rot;
+    const int at = row0 + t < a.n_rows ? a.positions[row0 + t] : -1;
+    float c = 1.f, s = 0.f;
+    if (at >= 0) rope_turn(at, r.turns[j], static_cast<float>(r.magnitude), c, s);
+    cs[i] = make_float2(c, a.inverse ? -s : s);
   }
   __syncthreads();
-  const T* x = static_cast<const T*>(a.x) + row * a.x_row;
-  T* out = static_cast<T*>(a.out) + row * a.out_row;
-  for (int i = threadIdx.x; i < a.n_heads * r.n_rot; i += kRopeOpThreads) {
-    const int h = i / r.n_rot, j = i % r.n_rot;
-    const int d0 = r.layout == SPEC_ROPE_HALF ? j : 2 * j;
-    const int d1 = r.layout == SPEC_ROPE_HALF ? j + r.span / 2 : 2 * j + 1;
-    const float x0 = rope_load(x + h * a.x_head + d0), x1 = rope_load(x + h * a.x_head + d1);
-    rope_store(out + h * a.out_head + d0, x0 * cs[j].x - x1 * cs[j].y);
-    rope_store(out + h * a.out_head + d1, x0 * cs[j].y + x1 * cs[j].x);
+}
+
+template <typename T, int LAYOUT>
+__global__ void __launch_bounds__(kRopeOpThreads) rope_direct_kernel(const __grid_constant__ RopeArgs r,
+                                                                     const __grid_constant__ RopeOpArgs a,
+                                                                     const __grid_constant__ RopePlan p) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr bool HALF = LAYOUT == SPEC_ROPE_HALF;
+  constexpr int B = HALF ? 2 : 4;          // units in flight of a thread: four 16-byte loads
+  extern __shared__ float2 cs[];
+  __shared__ int pos[kRopeRows];
+  pdl_trigger();
+  pdl_wait();
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_blocks) * p.rows;
+  const int h0 = (blockIdx.x % p.head_blocks) * p.heads, heads = min(p.heads, a.n_heads - h0);
+  const int n = p.rows * p.heads * p.units, pair_units = r.span / 2 / E;
+  for (int base = 0; base < n; base += B * kRopeOpThreads) {
+    Piece<T> x0[B], x1[B];
+    int row[B], d[B];                      // row in the CTA (-1: nothing to do), first dim
+    T* dst[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = base + b * kRopeOpThreads + threadIdx.x;
+      const int rh = p.by_units(i), u = i - rh * p.units, t = p.by_heads(rh), h = rh - t * p.heads;
+      row[b] = i < n && h < heads && row0 + t < a.n_rows ? t : -1;
+      // half: pairs of pieces first, then the pieces that pass through
+      d[b] = HALF && u >= pair_units ? r.span + (u - pair_units) * E : u * E;
+      if (row[b] < 0) continue;
+      const T* src = static_cast<const T*>(a.x) + (row0 + t) * a.x_row + (h0 + h) * a.x_head + d[b];
+      dst[b] = static_cast<T*>(a.out) + (row0 + t) * a.out_row + (h0 + h) * a.out_head + d[b];
+      x0[b].v = *reinterpret_cast<const uint4*>(src);
+      if (HALF && d[b] < r.span) x1[b].v = *reinterpret_cast<const uint4*>(src + r.span / 2);
+    }
+    if (base == 0) angles(r, a, p, row0, cs, pos);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (row[b] < 0 || pos[row[b]] < 0) continue;
+      const float2* c = cs + row[b] * r.n_rot;
+      if (HALF) {
+        if (d[b] < r.n_rot) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (d[b] + e < r.n_rot) turn(x0[b].e[e], x1[b].e[e], c[d[b] + e]);
+        }
+        if (d[b] < r.span) *reinterpret_cast<uint4*>(dst[b] + r.span / 2) = x1[b].v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+          if (d[b] / 2 + e < r.n_rot) turn(x0[b].e[2 * e], x0[b].e[2 * e + 1], c[d[b] / 2 + e]);
+      }
+      *reinterpret_cast<uint4*>(dst[b]) = x0[b].v;
+    }
   }
-  if (a.x == a.out) return;
-  for (int i = threadIdx.x; i < a.n_heads * a.dim; i += kRopeOpThreads) {
-    const int h = i / a.dim, d = i % a.dim;
-    const bool turned = r.layout == SPEC_ROPE_HALF
-                            ? d < r.n_rot || (d >= r.span / 2 && d < r.span / 2 + r.n_rot)
-                            : d < 2 * r.n_rot;
-    if (!turned) out[h * a.out_head + d] = x[h * a.x_head + d];
+}
+
+// Staged form; PIECES: 16 bytes at a time.
+template <typename T, bool PIECES>
+__global__ void __launch_bounds__(kRopeOpThreads) rope_staged_kernel(const __grid_constant__ RopeArgs r,
+                                                                     const __grid_constant__ RopeOpArgs a,
+                                                                     const __grid_constant__ RopePlan p) {
+  constexpr int E = PIECES ? 16 / sizeof(T) : 1;
+  extern __shared__ float2 cs[];
+  __shared__ int pos[kRopeRows];
+  __shared__ __align__(16) uint8_t tile_raw[kRopeTile];
+  T* tile = reinterpret_cast<T*>(tile_raw);
+  pdl_trigger();
+  pdl_wait();
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_blocks) * p.rows;
+  const int h0 = (blockIdx.x % p.head_blocks) * p.heads, heads = min(p.heads, a.n_heads - h0);
+  const int n = p.rows * p.heads * p.units;
+  auto each = [&](auto&& f) {              // every piece of the CTA's heads
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kRopeOpThreads) {
+      const int rh = p.by_units(i), u = i - rh * p.units, t = p.by_heads(rh), h = rh - t * p.heads;
+      if (h < heads && row0 + t < a.n_rows) f(i, t, h, u * E);
+    }
+  };
+  each([&](int i, int t, int h, int d) {
+    const T* src = static_cast<const T*>(a.x) + (row0 + t) * a.x_row + (h0 + h) * a.x_head + d;
+    if (PIECES) reinterpret_cast<uint4*>(tile)[i] = *reinterpret_cast<const uint4*>(src);
+    else tile[i] = *src;
+  });
+  angles(r, a, p, row0, cs, pos);
+  const bool half = r.layout == SPEC_ROPE_HALF;
+  for (int i = threadIdx.x; i < p.rows * p.heads * r.n_rot; i += kRopeOpThreads) {
+    const int rh = p.by_pairs(i), j = i - rh * r.n_rot, t = p.by_heads(rh);
+    T* x = tile + rh * a.dim;
+    turn(x[half ? j : 2 * j], x[half ? j + r.span / 2 : 2 * j + 1], cs[t * r.n_rot + j]);
   }
+  __syncthreads();
+  each([&](int i, int t, int h, int d) {
+    if (pos[t] < 0) return;
+    T* dst = static_cast<T*>(a.out) + (row0 + t) * a.out_row + (h0 + h) * a.out_head + d;
+    if (PIECES) *reinterpret_cast<uint4*>(dst) = reinterpret_cast<uint4*>(tile)[i];
+    else *dst = tile[i];
+  });
+}
+
+template <typename T>
+cudaError_t launch_typed(const RopeArgs& r, const RopeOpArgs& a, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(T);
+  const auto whole = [&](int64_t stride, int64_t count) { return count == 1 || stride % E == 0; };
+  const bool pieces = a.dim % E == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && whole(a.x_row, a.n_rows) &&
+                      whole(a.x_head, a.n_heads) && whole(a.out_row, a.n_rows) && whole(a.out_head, a.n_heads);
+  const bool half = r.layout == SPEC_ROPE_HALF;
+  const bool direct = pieces && (!half || (r.span / 2) % E == 0);
+  // bytes of a CTA: enough in flight for many rows, spread over the SMs for few
+  const int64_t head = static_cast<int64_t>(a.dim) * sizeof(T), total = head * a.n_heads * a.n_rows;
+  int64_t bytes = total / (2 * 148);
+  bytes = bytes < 4096 ? 4096 : bytes > kRopeTile ? kRopeTile : bytes;
+  RopePlan p{};
+  p.heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.n_heads, bytes / head)));
+  p.rows = p.heads < a.n_heads ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeRows, bytes / (head * a.n_heads))));
+  p.head_blocks = (a.n_heads + p.heads - 1) / p.heads;
+  p.units = !direct ? (pieces ? a.dim / E : a.dim) : half ? r.span / 2 / E + (a.dim - r.span) / E : a.dim / E;
+  if (direct && a.x == a.out)               // in place: only what turns
+    p.units = half ? (r.n_rot + E - 1) / E : (2 * r.n_rot + E - 1) / E;
+  if (p.units < 1) return cudaSuccess;
+  p.by_units = make_div(p.units);
+  p.by_heads = make_div(p.heads);
+  p.by_pairs = make_div(std::max(r.n_rot, 1));
+  const int64_t ctas = (static_cast<int64_t>(a.n_rows) + p.rows - 1) / p.rows * p.head_blocks;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(ctas)), block(kRopeOpThreads);
+  const size_t smem = static_cast<size_t>(p.rows) * r.n_rot * sizeof(float2);   // at most 32 KB
+  if (direct)
+    return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF>, grid, block, smem, st, r, a, p)
+                : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED>, grid, block, smem, st, r, a, p);
+  // the staged form's tile comes on top
+  auto kern = pieces ? rope_staged_kernel<T, true> : rope_staged_kernel<T, false>;
+  static std::atomic<uint64_t> allowed[2] = {};
+  const cudaError_t e = allow_smem(kern, kRopeRows * kMaxPairs * static_cast<int>(sizeof(float2)), allowed[pieces]);
+  return e != cudaSuccess ? e : launch_k(kern, grid, block, smem, st, r, a, p);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& r, const RopeOpArgs& a, int dtype, cudaStream_t st) {
-  const dim3 grid(a.n_rows), block(kRopeOpThreads);
-  if (dtype == SPEC_BF16) return launch_k(rope_kernel<uint16_t>, grid, block, 0, st, r, a);
-  if (dtype == SPEC_FP16) return launch_k(rope_kernel<__half>, grid, block, 0, st, r, a);
-  return launch_k(rope_kernel<float>, grid, block, 0, st, r, a);
+  if (dtype == SPEC_BF16) return launch_typed<uint16_t>(r, a, st);
+  if (dtype == SPEC_FP16) return launch_typed<__half>(r, a, st);
+  return launch_typed<float>(r, a, st);
 }
 
 }  // namespace sv
