@@ -68,13 +68,17 @@ int rope_args(const spec_rope_config* r, int head_dim, RopeArgs* a) {
   a->span = 2;
   a->magnitude = 1.0;
   if (!r) return SPEC_OK;
-  const int rc = rope_frequencies(r, head_dim, a->turns);
+  double f[kMaxPairs];
+  const int rc = rope_frequencies(r, head_dim, f);
   if (rc) return rc;
   a->layout = r->layout;
   a->span = r->span;
   a->n_rot = r->n_rot;
   a->magnitude = r->magnitude;
-  for (int j = 0; j < r->n_rot; ++j) a->turns[j] /= 2.0 * M_PI;
+  for (int j = 0; j < r->n_rot; ++j) {
+    const double turns = f[j] / (2.0 * M_PI);
+    a->step[j] = static_cast<uint64_t>(ldexp(turns - floor(turns), 64));   // below 2^64: the fraction is below 1
+  }
   return SPEC_OK;
 }
 

@@ -43,7 +43,7 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
   if (j < 0) return static_cast<float>(x);
   const double w = bf16_to_f32(p[e]);
   double c, s;
-  rope_turn(pos, r.turns[j], c, s);
+  rope_turn(pos, r.step[j], c, s);
   c *= r.magnitude;
   s *= r.magnitude;
   return to_odd(second ? w * s + x * c : x * c - w * s);
@@ -86,7 +86,9 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
   constexpr int LR = D / 8;                  // lanes of a row
   constexpr int RI = 32 / LR;                // rows of a warp at a time
   constexpr int IT = BT / (kWriteWarps * RI) > 0 ? BT / (kWriteWarps * RI) : 1;
-  extern __shared__ float2 cs[];             // [BT][n_tab], (1, 0) past the turned pairs; 8 times (1, 0)
+  // [BT][n_tab], (1, 0) past the turned pairs: two pairs next to each other, then those
+  // of the next lane (in pair order the lanes' reads met in the same banks); 8 (1, 0)
+  extern __shared__ float2 cs[];
   __shared__ uint32_t red[2][kWriteWarps];
   __shared__ int list_n;
   __shared__ int2 list[kWriteList];          // (head of the CTA, row, dim), the scale's inverse
@@ -128,14 +130,16 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
   const bool half = r.layout == SPEC_ROPE_HALF, turns_keys = !is_v && r.n_rot > 0;
   const int hs = r.span / 2;
   float2* none = cs + BT * n_tab;
+  const int lanes = half ? n_tab / 8 : n_tab / 4;   // that share a row's turned pairs
   if (turns_keys) {
     const int j = threadIdx.x % n_tab, step = kWriteThreads / n_tab;   // a thread's pair stays, its row advances
-    const double turn = j < r.n_rot ? r.turns[j] : 0.0;
+    const uint64_t turn = j < r.n_rot ? r.step[j] : 0;
+    const int at = half ? ((j % 8 / 2) * lanes + j / 8) * 2 + j % 2 : ((j % 4 / 2) * lanes + j / 4) * 2 + j % 2;
     if (threadIdx.x < 8) none[threadIdx.x] = make_float2(1.f, 0.f);
     for (int t = lo + threadIdx.x / n_tab; t < hi && threadIdx.x < step * n_tab; t += step) {
       float ca = 1.f, sa = 0.f;
       if (j < r.n_rot) rope_turn(p0 + t, turn, static_cast<float>(r.magnitude), ca, sa);
-      cs[t * n_tab + j] = make_float2(ca, sa);
+      cs[t * n_tab + at] = make_float2(ca, sa);
     }
   }
   // this lane's dims: pairs from j0 on (-1: they pass through); for half pairs the
@@ -181,14 +185,15 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
       }
       if (turns_keys) {
         // (dims that pass through turn by (1, 0), half pairs with themselves)
-        const float4* ct = reinterpret_cast<const float4*>(j0 >= 0 && (there >> i & 1) ? cs + (t0 + i * RI) * n_tab + j0 : none);
+        const float4* ct = reinterpret_cast<const float4*>(j0 >= 0 && (there >> i & 1) ? cs + (t0 + i * RI) * n_tab + (half ? j0 / 8 : j0 / 4) * 2 : none);
+        const int ce = j0 >= 0 && (there >> i & 1) ? lanes : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = __hmax2(top, abs2(w[e]));
         if (half) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t o = __shfl_sync(0xffffffffu, w[e], from) ^ flip;
-            const float4 q = ct[e];
+            const float4 q = ct[e * ce];
             with = __hmax2(with, abs2(o));
             y[i][2 * e] = fmaf(__uint_as_float(o << 16), q.y, y[i][2 * e] * q.x);
             y[i][2 * e + 1] = fmaf(__uint_as_float(o & 0xffff0000u), q.w, y[i][2 * e + 1] * q.z);
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
         } else {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float4 q = ct[e];
+            const float4 q = ct[e * ce];
             const float x0 = y[i][4 * e], x1 = y[i][4 * e + 1], x2 = y[i][4 * e + 2], x3 = y[i][4 * e + 3];
             y[i][4 * e] = x0 * q.x - x1 * q.y;
             y[i][4 * e + 1] = x0 * q.y + x1 * q.x;
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
   if (threadIdx.x < r.n_rot) {
     const int pos = min(max(L, 0), 1 << 30) + a.q_offset + i;
     float c, s;
-    rope_turn(pos, r.turns[threadIdx.x], static_cast<float>(r.magnitude), c, s);
+    rope_turn(pos, r.step[threadIdx.x], static_cast<float>(r.magnitude), c, s);
     cs[threadIdx.x] = make_float2(c, s);
   }
   __syncthreads();

@@ -28,32 +28,34 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done) {
   return f;
 }
 
-// A rotary configuration as the kernels take it: turns[j] = f_j / (2 pi), so
-// the angle's reduction is exact (a subtraction of a whole number).
+// A rotary configuration as the kernels take it: step[j] is f_j / (2 pi) turns
+// modulo 1, in units of 2^-64, so a position's fraction of a turn is a 64-bit product
+// that wraps.
 struct RopeArgs {
   int layout, span, n_rot;
   double magnitude;
-  double turns[kMaxPairs];
+  uint64_t step[kMaxPairs];
 };
 
-// (c, s) of pair j at a position, in binary64.  The product of a position
-// below 2^31 and a frequency is off by at most 2^-53 of itself.
-__device__ __forceinline__ void rope_turn(int pos, double turns, double& c, double& s) {
-  const double t = static_cast<double>(pos) * turns;
-  sincospi(2.0 * (t - rint(t)), &s, &c);
+// (c, s) of pair j at a position, in binary64.
+__device__ __forceinline__ void rope_turn(int pos, uint64_t step, double& c, double& s) {
+  const int64_t f = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * step);   // -1/2 .. 1/2 turn
+  sincospi(static_cast<double>(f) * 0x1p-63, &s, &c);
 }
 
-// magnitude * (cos, sin) in binary32: the turn's fraction is reduced in binary64
-// and split into a binary32 head and tail; the tail enters to first order, so
-// the results are off by little more than half a step.
-__device__ __forceinline__ void rope_turn(int pos, double turns, float magnitude, float& c, float& s) {
-  const double t = static_cast<double>(pos) * turns;
-  const double f = t - rint(t);
-  const float hi = static_cast<float>(f), lo = static_cast<float>(f - hi) * 6.2831853f;
+// magnitude * (cos, sin) in binary32: the fraction of a turn as a binary32 head of
+// 23 bits and a tail that enters to first order, so the results are off by little
+// more than half a step.  No binary64 and no conversions: those are at a fraction
+// of the other instructions' rate, and formed half of spec_rope's time.
+__device__ __forceinline__ void rope_turn(int pos, uint64_t step, float magnitude, float& c, float& s) {
+  const uint64_t f = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * step + (1ull << 63);
+  const uint32_t top = static_cast<uint32_t>(f >> 32), low = static_cast<uint32_t>(f >> 18);
+  const float head = __uint_as_float(0x3f800000u | top >> 9) - 1.5f;                        // steps of 2^-23
+  const float tail = (__uint_as_float(0x3f800000u | (low & 0x7fffffu)) - 1.f) * 0x1.921fb6p-21f;   // 2 pi 2^-23 of them
   float sh, ch;
-  sincospif(2.f * hi, &sh, &ch);
-  c = (ch - sh * lo) * magnitude;
-  s = (sh + ch * lo) * magnitude;
+  sincospif(2.f * head, &sh, &ch);
+  c = (ch - sh * tail) * magnitude;
+  s = (sh + ch * tail) * magnitude;
 }
 
 // ---------------------------------------------------------------- spec_rope

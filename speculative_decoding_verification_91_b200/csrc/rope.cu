@@ -42,7 +42,8 @@ Div make_div(int d) { return Div{static_cast<uint32_t>(d), static_cast<uint32_t>
 struct RopePlan {
   int rows, heads, head_blocks;   // of a CTA; CTAs across the heads
   int units;                      // pieces (direct) of a head
-  Div by_units, by_heads, by_pairs;
+  int n_tab;                      // n_rot, to whole pieces (direct)
+  Div by_units, by_heads, by_pairs, by_n;   // by_n: pieces of a row
 };
 
 template <typename T>
@@ -75,7 +76,10 @@ __device__ __forceinline__ void turn(T& a, T& b, float2 cs) {
   b = from_f<T>(x0 * cs.y + x1 * cs.x);
 }
 
-// Positions and (c, s) of the CTA's rows; ends with a barrier.
+// Positions and (c, s) of the CTA's rows; ends with a barrier.  PP pairs of a piece:
+// pair j of a row at [j % PP][j / PP], so that the lanes of a warp, a piece each, read
+// next to each other (in pair order the bank conflicts took half of the kernel's time).
+template <int PP>
 __device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, const RopePlan& p, int64_t row0,
                                        float2* cs, int* pos) {
   const int n = p.rows * r.n_rot;
@@ -85,62 +89,100 @@ __device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, c
     const int t = p.by_pairs(i), j = i - t * r.n_rot;
     const int at = row0 + t < a.n_rows ? a.positions[row0 + t] : -1;
     float c = 1.f, s = 0.f;
-    if (at >= 0) rope_turn(at, r.turns[j], static_cast<float>(r.magnitude), c, s);
-    cs[i] = make_float2(c, a.inverse ? -s : s);
+    if (at >= 0) rope_turn(at, r.step[j], static_cast<float>(r.magnitude), c, s);
+    cs[t * p.n_tab + (PP == 1 ? j : j % PP * (p.n_tab / PP) + j / PP)] = make_float2(c, a.inverse ? -s : s);
   }
   __syncthreads();
 }
 
+// A thread keeps its piece (or two opposite ones) of a head and goes down the CTA's
+// rows, so that what depends on the piece is formed once.
 template <typename T, int LAYOUT>
 __global__ void __launch_bounds__(kRopeOpThreads) rope_direct_kernel(const __grid_constant__ RopeArgs r,
                                                                      const __grid_constant__ RopeOpArgs a,
                                                                      const __grid_constant__ RopePlan p) {
   constexpr int E = 16 / sizeof(T);
   constexpr bool HALF = LAYOUT == SPEC_ROPE_HALF;
-  constexpr int B = HALF ? 2 : 4;          // units in flight of a thread: four 16-byte loads
+  constexpr int B = HALF ? 2 : 4;          // rows in flight of a thread: four 16-byte loads
+  constexpr int PP = HALF ? E : E / 2;     // pairs of a piece
   extern __shared__ float2 cs[];
   __shared__ int pos[kRopeRows];
   pdl_trigger();
   pdl_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_blocks) * p.rows;
   const int h0 = (blockIdx.x % p.head_blocks) * p.heads, heads = min(p.heads, a.n_heads - h0);
-  const int n = p.rows * p.heads * p.units, pair_units = r.span / 2 / E;
-  for (int base = 0; base < n; base += B * kRopeOpThreads) {
-    Piece<T> x0[B], x1[B];
-    int row[B], d[B];                      // row in the CTA (-1: nothing to do), first dim
-    T* dst[B];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int i = base + b * kRopeOpThreads + threadIdx.x;
-      const int rh = p.by_units(i), u = i - rh * p.units, t = p.by_heads(rh), h = rh - t * p.heads;
-      row[b] = i < n && h < heads && row0 + t < a.n_rows ? t : -1;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), a.n_rows - row0));
+  const int n = p.heads * p.units, pair_units = r.span / 2 / E;
+  // threads side by side on a row's pieces, `side` rows at a time
+  const int side = n < kRopeOpThreads ? p.by_n(kRopeOpThreads) : 1;
+  const int t0 = n < kRopeOpThreads ? p.by_n(threadIdx.x) : 0;
+  int i = threadIdx.x - t0 * n, t = t0, d = 0, j = 0;
+  const T* src = nullptr;
+  T* dst = nullptr;
+  bool turns = false, pair = false;
+  auto piece = [&]() -> bool {             // what depends on the piece; false: none left
+    for (; i < n && t0 < side; i += kRopeOpThreads) {
+      const int h = p.by_units(i), u = i - h * p.units;
+      if (h >= heads) continue;
       // half: pairs of pieces first, then the pieces that pass through
-      d[b] = HALF && u >= pair_units ? r.span + (u - pair_units) * E : u * E;
-      if (row[b] < 0) continue;
-      const T* src = static_cast<const T*>(a.x) + (row0 + t) * a.x_row + (h0 + h) * a.x_head + d[b];
-      dst[b] = static_cast<T*>(a.out) + (row0 + t) * a.out_row + (h0 + h) * a.out_head + d[b];
-      x0[b].v = *reinterpret_cast<const uint4*>(src);
-      if (HALF && d[b] < r.span) x1[b].v = *reinterpret_cast<const uint4*>(src + r.span / 2);
+      pair = HALF && u < pair_units;
+      d = HALF && !pair ? r.span + (u - pair_units) * E : u * E;
+      j = HALF ? d : d / 2;
+      turns = (!HALF || pair) && j < r.n_rot;
+      src = static_cast<const T*>(a.x) + (row0 + t0) * a.x_row + (h0 + h) * a.x_head + d;
+      dst = static_cast<T*>(a.out) + (row0 + t0) * a.out_row + (h0 + h) * a.out_head + d;
+      t = t0;
+      return t < rows;
     }
-    if (base == 0) angles(r, a, p, row0, cs, pos);
+    return false;
+  };
+  Piece<T> x0[B], x1[HALF ? B : 1];
+  auto load = [&]() {
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      if (row[b] < 0 || pos[row[b]] < 0) continue;
-      const float2* c = cs + row[b] * r.n_rot;
-      if (HALF) {
-        if (d[b] < r.n_rot) {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (d[b] + e < r.n_rot) turn(x0[b].e[e], x1[b].e[e], c[d[b] + e]);
-        }
-        if (d[b] < r.span) *reinterpret_cast<uint4*>(dst[b] + r.span / 2) = x1[b].v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-          if (d[b] / 2 + e < r.n_rot) turn(x0[b].e[2 * e], x0[b].e[2 * e + 1], c[d[b] / 2 + e]);
-      }
-      *reinterpret_cast<uint4*>(dst[b]) = x0[b].v;
+      if (t + b * side >= rows) break;
+      x0[b].v = __ldcs(reinterpret_cast<const uint4*>(src + b * side * a.x_row));
+      if (HALF && pair) x1[b].v = __ldcs(reinterpret_cast<const uint4*>(src + b * side * a.x_row + r.span / 2));
     }
+  };
+  bool some = piece();
+  if (some) load();
+  angles<PP>(r, a, p, row0, cs, pos);
+  while (some) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int tb = t + b * side;
+      if (tb >= rows) break;
+      if (turns) {
+        const float2* c = cs + tb * p.n_tab + j / PP;
+        const int ce = p.n_tab / PP;       // from a piece's pair to its next
+        if (j + PP <= r.n_rot) {
+#pragma unroll
+          for (int e = 0; e < PP; ++e) {
+            if (HALF) turn(x0[b].e[e], x1[b].e[e], c[e * ce]);
+            else turn(x0[b].e[2 * e], x0[b].e[2 * e + 1], c[e * ce]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < PP; ++e) {
+            if (j + e >= r.n_rot) break;
+            if (HALF) turn(x0[b].e[e], x1[b].e[e], c[e * ce]);
+            else turn(x0[b].e[2 * e], x0[b].e[2 * e + 1], c[e * ce]);
+          }
+        }
+      }
+      if (pos[tb] < 0) continue;
+      *reinterpret_cast<uint4*>(dst + b * side * a.out_row) = x0[b].v;
+      if (HALF && pair) *reinterpret_cast<uint4*>(dst + b * side * a.out_row + r.span / 2) = x1[b].v;
+    }
+    t += B * side;
+    src += B * side * a.x_row;
+    dst += B * side * a.out_row;
+    if (t >= rows) {
+      i += kRopeOpThreads;
+      some = piece();
+    }
+    if (some) load();
   }
 }
 
@@ -171,7 +213,7 @@ __global__ void __launch_bounds__(kRopeOpThreads) rope_staged_kernel(const __gri
     if (PIECES) reinterpret_cast<uint4*>(tile)[i] = *reinterpret_cast<const uint4*>(src);
     else tile[i] = *src;
   });
-  angles(r, a, p, row0, cs, pos);
+  angles<1>(r, a, p, row0, cs, pos);
   const bool half = r.layout == SPEC_ROPE_HALF;
   for (int i = threadIdx.x; i < p.rows * p.heads * r.n_rot; i += kRopeOpThreads) {
     const int rh = p.by_pairs(i), j = i - rh * r.n_rot, t = p.by_heads(rh);
@@ -199,7 +241,8 @@ cudaError_t launch_typed(const RopeArgs& r, const RopeOpArgs& a, cudaStream_t st
   // bytes of a CTA: enough in flight for many rows, spread over the SMs for few
   const int64_t head = static_cast<int64_t>(a.dim) * sizeof(T), total = head * a.n_heads * a.n_rows;
   int64_t bytes = total / (2 * 148);
-  bytes = bytes < 4096 ? 4096 : bytes > kRopeTile ? kRopeTile : bytes;
+  const int64_t most = direct ? 2 * kRopeTile : kRopeTile;
+  bytes = bytes < 4096 ? 4096 : bytes > most ? most : bytes;
   RopePlan p{};
   p.heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.n_heads, bytes / head)));
   p.rows = p.heads < a.n_heads ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeRows, bytes / (head * a.n_heads))));
@@ -210,11 +253,14 @@ cudaError_t launch_typed(const RopeArgs& r, const RopeOpArgs& a, cudaStream_t st
   if (p.units < 1) return cudaSuccess;
   p.by_units = make_div(p.units);
   p.by_heads = make_div(p.heads);
+  p.by_n = make_div(p.heads * p.units);
   p.by_pairs = make_div(std::max(r.n_rot, 1));
   const int64_t ctas = (static_cast<int64_t>(a.n_rows) + p.rows - 1) / p.rows * p.head_blocks;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ctas)), block(kRopeOpThreads);
-  const size_t smem = static_cast<size_t>(p.rows) * r.n_rot * sizeof(float2);   // at most 32 KB
+  const int pp = !direct ? 1 : half ? E : E / 2;
+  p.n_tab = (r.n_rot + pp - 1) / pp * pp;
+  const size_t smem = static_cast<size_t>(p.rows) * p.n_tab * sizeof(float2);   // at most 32 KB
   if (direct)
     return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF>, grid, block, smem, st, r, a, p)
                 : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED>, grid, block, smem, st, r, a, p);
