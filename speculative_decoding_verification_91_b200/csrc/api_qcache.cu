@@ -137,6 +137,12 @@ bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_page
   if (s->n_splits > kMaxQSplits) return false;
   const uint64_t rows = (uint64_t)B * n * n_q_heads;     // (sequence, KV head, row)
   if (rows > 0x3fffffffull) return false;
+  // what the kernels count and divide in 32 bits: rows of a KV head by its query
+  // heads, and the key blocks of all (sequence, KV head, row block)
+  const uint64_t G = n_q_heads / c->n_kv_heads, per_head = n * G;
+  if (per_head * G > 0xffffffffull ||
+      (uint64_t)B * c->n_kv_heads * ((per_head + 31) / 32) * ((uint64_t)max_pages / 2 + 1) > 0x7fffffffull)
+    return false;
   const uint64_t slots = rows * s->n_splits, D = c->head_dim;
   size_t off = kWsHeaderBytes;
   s->codes = off;   off = up256(off + 2 * rows * D);
@@ -254,6 +260,8 @@ int run_attn(const spec_qcache* c, const RopeArgs& r, const AttnCall& k, const A
   a.kv_extra = k.kv_extra;
   a.window = k.window;
   a.split = s.split;
+  a.by_split = make_div(s.split / kQBlk);   // up to 2^7 of at most 2^23 blocks
+  a.by_G = make_div(a.G);
   a.n_splits = s.n_splits;
   a.q = static_cast<const uint16_t*>(k.q);
   a.q_row = k.q_row;

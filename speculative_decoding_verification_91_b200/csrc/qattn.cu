@@ -137,21 +137,21 @@ struct Walker {
   int b, h, rb, sidx, L;
   int split0, p0, p1;      // the sequence's first split; positions of the row block's first and last row
   SeqKeys k;
-  long base, end, pos;     // key blocks before (b, h, rb); where the CTA stops; this item's start
+  int base, end, pos;      // key blocks before (b, h, rb); where the CTA stops; this item's start
   int lo, hi, blk0, nb;    // this item's keys and blocks (nb = 0: none)
   bool fresh;
   __device__ bool valid() const { return b < a->B && pos < end; }
-  __device__ void load_seq() {
-    L = a->c.seq_lens[b];
+  __device__ void load_seq(int len) {
+    L = len;
     k = seq_keys(*a, L);
-    split0 = k.lo / a->split;
+    split0 = a->by_split(k.lo >> kLgBlk);
   }
   // from the first split of (b, h, rb) that is wanted: its rows, then its keys
   __device__ void derive(bool rows) {
     if (rows) {
       const int r0 = rb * RP, r1 = min(a->rows, r0 + RP) - 1;
-      p0 = L + a->q_offset + r0 / a->G;
-      p1 = L + a->q_offset + r1 / a->G;
+      p0 = L + a->q_offset + a->by_G(r0);
+      p1 = L + a->q_offset + a->by_G(r1);
       fresh = true;
     }
     const int s0 = (split0 + sidx) * a->split, start = max(s0, k.lo);
@@ -173,7 +173,7 @@ struct Walker {
           h = 0;
           do {
             if (++b >= a->B) return;
-            load_seq();
+            load_seq(a->c.seq_lens[b]);
           } while (k.blocks == 0);
         }
       }
@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   uint64_t* p_full = s_free + 2;                           // [2] by block parity
   uint64_t* pv_done = p_full + 2;                          // [2]
   uint64_t* it_full = pv_done + 2;                         // [kItems] by item
-  uint64_t* it_empty = it_full + kItems;                   // [kItems]
+  uint64_t* sc_full = it_full + kItems;                    // [kItems] its scales
+  uint64_t* it_empty = sc_full + kItems;                   // [kItems]
   uint64_t* q_ready = it_empty + kItems;
   uint64_t* o_free = q_ready + 1;
   uint64_t* mma_done = o_free + 1;
@@ -252,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
+      mbar_init(&sc_full[i], 1);
       mbar_init(&it_empty[i], kSoftWarps + 2);
     }
     mbar_init(q_ready, kSoftWarps);
@@ -404,57 +406,51 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     // --------------------------------------------------- items and scales
     const int RB = (a.rows + RP - 1) / RP, per_b = a.c.n_kv_heads * RB;
     // this CTA's share [x0, x1) of all key blocks and its first item
-    long total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      long n = 0;
-      if (b0 + lane < a.B) {
-        const int L = a.c.seq_lens[b0 + lane];
-        n = seq_keys(a, L).blocks;
-        if (blockIdx.x == 0 &&
-            (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * kPg))
-          flag_status(a.c.status, SPEC_DEV_BAD_LENGTH);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-      total += n * per_b;
+    const auto length = [&](int b) { return b < a.B ? a.c.seq_lens[b] : 0; };
+    const auto blocks = [&](int b, int L) { return b < a.B ? seq_keys(a, L).blocks * per_b : 0; };
+    int L = length(lane), n = blocks(lane, L), total = 0;
+    for (int b = lane; b - lane < a.B; b += 32) {
+      if (b >= 32) n = blocks(b, L = length(b));
+      if (blockIdx.x == 0 && b < a.B &&
+          (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * kPg))
+        flag_status(a.c.status, SPEC_DEV_BAD_LENGTH);
+      total += __reduce_add_sync(0xffffffffu, n);
     }
-    const long x0 = static_cast<long>(blockIdx.x) * total / gridDim.x;
-    const long x1 = static_cast<long>(blockIdx.x + 1) * total / gridDim.x;
+    const int me = blockIdx.x, per = total / gridDim.x, rest = total % gridDim.x;
+    const int x0 = me * per + min(me, rest), x1 = x0 + per + (me < rest ? 1 : 0);
     Walker w{};
     w.a = &a;
     w.RP = RP;
     w.RB = RB;
     w.b = a.B;
     w.end = x1;
-    long pre = 0;
-    for (int b0 = 0; b0 < a.B && w.b == a.B && x1 > x0; b0 += 32) {
-      long n = 0;
-      if (b0 + lane < a.B) n = static_cast<long>(seq_keys(a, a.c.seq_lens[b0 + lane]).blocks) * per_b;
-      long incl = n;
+    int pre = 0;
+    for (int b = lane; b - lane < a.B && w.b == a.B && x1 > x0; b += 32) {
+      if (a.B > 32) n = blocks(b, L = length(b));
+      int incl = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const long o = __shfl_up_sync(0xffffffffu, incl, off);
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += o;
       }
-      const long excl = pre + incl - n;
+      const int excl = pre + incl - n;
       const unsigned bal = __ballot_sync(0xffffffffu, n > 0 && x0 >= excl && x0 < excl + n);
       if (bal) {
         const int src = __ffs(bal) - 1;
-        w.b = b0 + src;
+        w.b = b - lane + src;
         w.base = __shfl_sync(0xffffffffu, excl, src);
+        w.load_seq(__shfl_sync(0xffffffffu, L, src));
       }
       pre += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (w.b < a.B) {
-      w.load_seq();
-      const long rem = x0 - w.base;
-      const int hr = static_cast<int>(rem / w.k.blocks), r = static_cast<int>(rem % w.k.blocks);
+      const int rem = x0 - w.base, hr = rem / w.k.blocks, r = rem - hr * w.k.blocks;
       w.h = hr / RB;
-      w.rb = hr % RB;
-      w.base += static_cast<long>(hr) * w.k.blocks;
+      w.rb = hr - w.h * RB;
+      w.base += hr * w.k.blocks;
       // the first split that starts at or after block r of the sequence
       const int first = w.k.lo >> kLgBlk, bps = a.split >> kLgBlk;
-      w.sidx = r == 0 ? 0 : (r + first + bps - 1) / bps - w.split0;
+      w.sidx = r == 0 ? 0 : static_cast<int>(a.by_split(r + first + bps - 1)) - w.split0;
       if (w.sidx < w.k.splits) {
         w.derive(true);
       } else {
@@ -501,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         x.page0 = static_cast<long>(w.b) * a.c.max_pages;
         x.out0 = static_cast<long>(w.b) * a.n;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_full[q]);      // the copies may start; the scales follow
       if (!end) {
         fresh = false;
         const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
@@ -523,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&it_full[q]);
+      if (lane == 0) mbar_arrive(&sc_full[q]);
       if (end || *fail) break;
       ++i;
     }
@@ -557,29 +555,32 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       if (x.nb < 0) return false;
       if (!x.fresh) return true;
       const bool have = row < x.nrows;
-      const int r = x.r0 + row, i_pos = r / a.G;
+      const int r = x.r0 + row, i_pos = a.by_G(r);
       p = x.p0 + i_pos;
       const long at = x.q_row + row, plane = static_cast<long>(a.B) * a.c.n_kv_heads * a.rows;
-      qs = have ? a.q_scale[at] : 0.f;
-      bad_q = qs != qs;                               // a NaN row's result is set at the end
-      qs = bad_q ? 0.f : qs * a.scale_log2;
-#pragma unroll 1
+      const float scale = have ? __ldcg(&a.q_scale[at]) : 0.f;
+      uint32_t v[2][D / 32][4];                       // all loads in flight at once
+#pragma unroll
       for (int c = 0; c < 2; ++c) {
         const uint4* src = reinterpret_cast<const uint4*>(a.q_codes + (at + c * plane) * D + cg * (D / 2));
-        uint32_t v[D / 32][4];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
           const uint4 z = have ? __ldcg(src + e) : make_uint4(0, 0, 0, 0);
-          v[e][0] = z.x;
-          v[e][1] = z.y;
-          v[e][2] = z.z;
-          v[e][3] = z.w;
+          v[c][e][0] = z.x;
+          v[c][e][1] = z.y;
+          v[c][e][2] = z.z;
+          v[c][e][3] = z.w;
         }
-        __syncwarp();
+      }
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < D / 64; ++e)
-          tmem_st8(t_lane + C::kColQ + c * (D / 4) + cg * (D / 8) + e * 8, *reinterpret_cast<uint32_t(*)[8]>(v[2 * e]));
-      }
+          tmem_st8(t_lane + C::kColQ + c * (D / 4) + cg * (D / 8) + e * 8,
+                   *reinterpret_cast<uint32_t(*)[8]>(v[c][2 * e]));
+      bad_q = scale != scale;                         // a NaN row's result is set at the end
+      qs = bad_q ? 0.f : scale * a.scale_log2;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -598,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const int row_lo = max(x_lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(x_hi, p);
       const float* ks = ks_s + (item % kItems) * kMaxScales;
       const float* vs = vs_s + (item % kItems) * kMaxScales;
+      wait(&sc_full[item % kItems], (item / kItems) & 1);
       float mref = kNoKey, l = 0.f;
       for (int j = 0; j < nb; ++j, ++g) {
         const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;

@@ -28,6 +28,13 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done) {
   return f;
 }
 
+// i / d for i * d < 2^32: mul = floor(2^32 / d) + 1
+struct Div {
+  uint32_t d, mul;
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1 ? i : __umulhi(i, mul); }
+};
+inline Div make_div(int d) { return Div{static_cast<uint32_t>(d), static_cast<uint32_t>((1ull << 32) / d) + 1}; }
+
 // A rotary configuration as the kernels take it: step[j] is f_j / (2 pi) turns
 // modulo 1, in units of 2^-64, so a position's fraction of a turn is a 64-bit product
 // that wraps.
@@ -95,6 +102,7 @@ struct QAttnArgs {
   QCacheArgs c;
   int B, n, G, rows;            // rows = n * G per (sequence, KV head)
   int q_offset, kv_extra, window, split, n_splits;
+  Div by_split, by_G;           // of key blocks by those of a split; of rows by G
   const uint16_t* q;
   int64_t q_row;
   float scale_log2;             // softmax scale * log2(e)
@@ -115,7 +123,7 @@ __device__ __forceinline__ SeqKeys seq_keys(const QAttnArgs& a, int L) {
   k.hi = min(L + a.kv_extra - 1, L + a.q_offset + a.n - 1);
   k.lo = a.window > 0 ? max(0, L + a.q_offset - a.window + 1) : 0;
   if (k.hi < k.lo) return k;
-  k.splits = k.hi / a.split - k.lo / a.split + 1;
+  k.splits = a.by_split(k.hi / kQBlk) - a.by_split(k.lo / kQBlk) + 1;
   k.blocks = k.hi / kQBlk - k.lo / kQBlk + 1;
   return k;
 }

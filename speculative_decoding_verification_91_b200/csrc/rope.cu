@@ -32,13 +32,6 @@ constexpr int kRopeOpThreads = 256;
 constexpr int kRopeRows = 32;           // rows of a CTA
 constexpr int kRopeTile = 16384;        // bytes of heads of a CTA
 
-// i / d for i, d < 65536: mul = floor(2^32 / d) + 1 (d = 1: handled apart)
-struct Div {
-  uint32_t d, mul;
-  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1 ? i : __umulhi(i, mul); }
-};
-Div make_div(int d) { return Div{static_cast<uint32_t>(d), static_cast<uint32_t>((1ull << 32) / d) + 1}; }
-
 struct RopePlan {
   int rows, heads, head_blocks;   // of a CTA; CTAs across the heads
   int units;                      // pieces (direct) of a head
