@@ -118,10 +118,22 @@ int call_split(const spec_qcache* c, int n_q_heads, int64_t B, int n, int max_pa
   const int cap = 256 * c->block_tokens;
   const int64_t rows = (int64_t)(n_q_heads / c->n_kv_heads) * n;
   const int64_t groups = B * c->n_kv_heads * ((rows + 63) / 64);
-  const int64_t want = (kItemsWanted + groups - 1) / groups, T = (int64_t)max_pages * SPEC_PAGE_SIZE;
-  int64_t e = ((T + want - 1) / want + kSplitGrain - 1) / kSplitGrain * kSplitGrain;
-  if (e < split) e = split;
-  return (int)(e < cap ? e : cap);
+  const int64_t most = (kItemsWanted + groups - 1) / groups, T = (int64_t)max_pages * SPEC_PAGE_SIZE;
+  int64_t best = 0, least = INT64_MAX;
+  for (int64_t w = 1; w <= most; ++w) {
+    int64_t e = ((T + w - 1) / w + kSplitGrain - 1) / kSplitGrain * kSplitGrain;
+    if (e < split) e = split;
+    if (e > cap) e = cap;
+    // key blocks of the busiest SM, two more an item, and the join: 1/40 block an item
+    const int64_t parts = (T + e - 1) / e;
+    const int64_t cost = (groups * parts + 147) / 148 * (e / kQBlk + 2) + (parts > 1 ? groups * parts / 40 : 0);
+    if (cost < least) {
+      least = cost;
+      best = e;
+    }
+    if (e == split) break;
+  }
+  return (int)best;
 }
 
 // False where the counts are out of range.

@@ -817,123 +817,168 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row.
 // The partials of the rq <= 16 rows of a group (a lane quadrant of the split
-// kernel) lie [dim][row].  A CTA takes 16 V dims of a group, a thread V of them of
-// one row; it keeps four sums by split index mod 4, each in ascending order, and
-// adds them in the order of the absolute index.  Splits without a key of the row
-// add nothing at fixed places, so the order does not depend on where the list of
-// splits starts, and V and U change nothing.  The time is a chain of memory
-// latencies: the sequence's length, the references and the first U splits'
-// partials are all asked for at once, those beyond the sequence's last split
-// (whatever the workspace holds) are dropped.
-constexpr int kJoinTile = 128;             // splits whose weights are held at a time
-template <int V, int U>
-__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a, int rq) {
-  __shared__ float w_s[kJoinTile][16], l_s[kJoinTile][16], m_s[16][16];
-  __shared__ float y_s[16][16 * V + 1];
+// kernel) lie [dim][row], and a thread takes V of a run of dims for one row.  Four
+// sums are kept by split index mod 4, each in ascending order, and added in the
+// order of the absolute index: by one thread (P = 1) or by four (P = 4), which
+// changes no bit, nor do V and U.  Splits without a key of the row add nothing at
+// fixed places, so the order does not depend on where the list of splits starts.
+// The time is a chain of memory latencies: the sequence's length, the references
+// and the first P U splits' partials are all asked for at once, those beyond the
+// sequence's last split (whatever the workspace holds) are dropped.
+template <int P, int V, int U>
+__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a, int rq, int runs) {
+  constexpr int NT = 256 / P, NA = 4 / P;
+  constexpr int kTile = P * U < 16 ? 16 : P * U;   // splits whose weights are held at a time
+  __shared__ float w_s[kTile][16], l_s[kTile][16], m_s[16][16];
+  __shared__ float y_s[P][16 + NT * V], d_s[P][16];
   pdl_trigger();
   pdl_wait();
-  const int D = a.c.dim, runs = D / (16 * V), groups = (a.rows + rq - 1) / rq;
+  const int D = a.c.dim, groups = (a.rows + rq - 1) / rq;
   const int run = blockIdx.x % runs, bhg = blockIdx.x / runs, grp = bhg % groups, bh = bhg / groups;
   const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads;
-  const int row = threadIdx.x & 15, tc = threadIdx.x >> 4;
   const int r0 = grp * rq, nr = min(rq, a.rows - r0);
+  const int dt = NT / nr, dims = dt * V, d0 = run * dims;    // dims next to each other in threads; of the run
+  if (d0 >= D) return;                                       // (groups of few rows need fewer runs)
   const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r0;
   const int L = a.c.seq_lens[b];
-  const bool mine = row < nr;
-  const float qs = mine ? a.q_scale[static_cast<int64_t>(bh) * a.rows + r0 + row] : 0.f;
-  const float* po = a.part_o + slot0 * D + static_cast<int64_t>(run * 16 * V + tc) * nr + row;
+  const int p = threadIdx.x / NT, el = threadIdx.x % NT, row = el % nr, td = el / nr;
+  const bool mine = td < dt;
+  const int trow = threadIdx.x & 15, ts = threadIdx.x >> 4;  // of the references: row, split
+  const float* po = a.part_o + slot0 * D + p * static_cast<int64_t>(a.rows) * D + (d0 + td) * nr + row;
   const int64_t step = static_cast<int64_t>(a.rows) * D;
+  bool want[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) want[v] = mine && d0 + td + dt * v < D;
   float x[U][V];
   auto load = [&](int s0) {
+    const float* at = po + s0 * step;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u, at += P * step)
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        x[u][v] = mine && s0 + u < a.n_splits ? __ldcg(po + (s0 + u) * step + 16 * v * nr) : 0.f;
+        x[u][v] = want[v] && s0 + P * u + p < a.n_splits ? __ldcg(at + dt * v * nr) : 0.f;
   };
   auto load_tile = [&](int s0) {                   // references into w_s, sums into l_s
-    float2 ml[kJoinTile / 16];
+    float2 ml[kTile / 16];
 #pragma unroll
-    for (int i = 0; i < kJoinTile / 16; ++i) {
-      const int s = s0 + i * 16 + tc;
-      ml[i] = mine && s < a.n_splits ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + row])
-                                     : make_float2(kNoKey, 0.f);
+    for (int i = 0; i < kTile / 16; ++i) {
+      const int s = s0 + i * 16 + ts;
+      ml[i] = trow < nr && s < a.n_splits ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + trow])
+                                          : make_float2(kNoKey, 0.f);
     }
 #pragma unroll
-    for (int i = 0; i < kJoinTile / 16; ++i) {
-      w_s[i * 16 + tc][row] = ml[i].x;
-      l_s[i * 16 + tc][row] = ml[i].y;
+    for (int i = 0; i < kTile / 16; ++i) {
+      w_s[i * 16 + ts][trow] = ml[i].x;
+      l_s[i * 16 + ts][trow] = ml[i].y;
     }
   };
   load(0);
+  const float qs = __ldcg(&a.q_scale[static_cast<int64_t>(bh) * a.rows + r0 + row]);
   load_tile(0);
   const SeqKeys k = seq_keys(a, L);
   float M = kNoKey;
-  for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
+  for (int s0 = 0; s0 < k.splits; s0 += kTile) {
     if (s0 > 0) load_tile(s0);                     // each thread reads back what it wrote
-    for (int s = tc; s < min(kJoinTile, k.splits - s0); s += 16) M = fmaxf(M, w_s[s][row]);
+    for (int s = ts; s < min(kTile, k.splits - s0); s += 16) M = fmaxf(M, w_s[s][trow]);
   }
-  m_s[tc][row] = M;
+  m_s[ts][trow] = M;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) M = fmaxf(M, m_s[i][row]);
-  float acc[4][V], den[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 16; ++i) M = fmaxf(M, m_s[i][trow]);
+  float acc[NA][V], den[NA];
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
+  for (int q = 0; q < NA; ++q) {
+    den[q] = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[p][v] = 0.f;
-  for (int s0 = 0; s0 < k.splits; s0 += kJoinTile) {
-    const int ns = min(kJoinTile, k.splits - s0);
-    if (k.splits > kJoinTile) {
+    for (int v = 0; v < V; ++v) acc[q][v] = 0.f;
+  }
+  for (int s0 = 0; s0 < k.splits; s0 += kTile) {
+    const int ns = min(kTile, k.splits - s0);
+    if (k.splits > kTile) {
       __syncthreads();
       load_tile(s0);
     }
-    for (int s = tc; s < ns; s += 16) {
-      const float m = w_s[s][row];
-      w_s[s][row] = m <= kNoKey ? 0.f : exp2f(m - M);
+    for (int s = ts; s < ns; s += 16) {
+      const float m = w_s[s][trow];
+      w_s[s][trow] = m <= kNoKey ? 0.f : exp2f(m - M);
     }
     __syncthreads();
-    for (int u0 = 0; u0 < ns; u0 += U) {
+    for (int u0 = 0; u0 < ns; u0 += P * U) {
       if (s0 + u0 > 0) load(s0 + u0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float w = u0 + u < ns ? w_s[u0 + u][row] : 0.f;
+        const int s = u0 + P * u + p;
+        const float w = s < ns ? w_s[s][row] : 0.f;
         if (w > 0.f) {                             // (a split without keys of the row has no sums)
-          den[u & 3] = fmaf(w, l_s[u0 + u][row], den[u & 3]);
+          den[u % NA] = fmaf(w, l_s[s][row], den[u % NA]);
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[u & 3][v] = fmaf(w, x[u][v], acc[u & 3][v]);
+          for (int v = 0; v < V; ++v) acc[u % NA][v] = fmaf(w, x[u][v], acc[u % NA][v]);
         }
       }
     }
   }
   // the four sums in the order of the absolute split index
-  const int turn = k.splits ? (k.lo / a.split) & 3 : 0;
+  const int turn = k.splits ? a.by_split(k.lo / kBlk) & 3 : 0;
   auto ordered = [&](const float(&q)[4]) {
     float z[4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-      z[p] = turn == 0 ? q[p] : turn == 1 ? q[(p + 3) & 3] : turn == 2 ? q[(p + 2) & 3] : q[(p + 1) & 3];
+    for (int i = 0; i < 4; ++i)
+      z[i] = turn == 0 ? q[i] : turn == 1 ? q[(i + 3) & 3] : turn == 2 ? q[(i + 2) & 3] : q[(i + 1) & 3];
     return ((z[0] + z[1]) + z[2]) + z[3];
   };
-  const float l = ordered(den);
+  // [row][dim] of the run, each row's dims next to each other
+  if (P == 1) {
+    if (mine) {
+      const float l = ordered(reinterpret_cast<const float(&)[4]>(den));
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float q[4] = {acc[0][v], acc[1][v], acc[2][v], acc[3][v]};
-    const float y = ordered(q);
-    y_s[row][tc + 16 * v] = l == 0.f ? 0.f : qs == qs ? y / l : qs;   // no key: zero
-  }
-  __syncthreads();
-  const int orow = threadIdx.x >> 4, q_row = r0 + orow, c = (threadIdx.x & 15) * V;
-  if (orow >= nr) return;
-  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + q_row / a.G) * (a.c.n_kv_heads * a.G) + h * a.G + q_row % a.G) * D +
-                  run * 16 * V + c;
-  if (V == 1) {
-    dst[0] = f32_to_bf16(y_s[orow][c]);
+      for (int v = 0; v < V; ++v) {
+        const float q[4] = {acc[0][v], acc[NA > 1 ? 1 : 0][v], acc[NA > 2 ? 2 : 0][v], acc[NA > 3 ? 3 : 0][v]};
+        const float y = ordered(q);
+        y_s[0][row * dims + td + dt * v] = l == 0.f ? 0.f : qs == qs ? y / l : qs;   // no key: zero
+      }
+    }
+    __syncthreads();
   } else {
+    if (mine) {
+      if (td == 0) d_s[p][row] = den[0];
 #pragma unroll
-    for (int v = 0; v < V; v += 2)
-      *reinterpret_cast<uint32_t*>(dst + v) = pack_bf16x2(y_s[orow][c + v], y_s[orow][c + v + 1]);
+      for (int v = 0; v < V; ++v) y_s[p][row * dims + td + dt * v] = acc[0][v];
+    }
+    __syncthreads();
+    if (p == 0 && mine) {
+      const float dq[4] = {d_s[0][row], d_s[P > 1 ? 1 : 0][row], d_s[P > 2 ? 2 : 0][row], d_s[P > 3 ? 3 : 0][row]};
+      const float l = ordered(dq);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = row * dims + td + dt * v;
+        const float q[4] = {y_s[0][i], y_s[P > 1 ? 1 : 0][i], y_s[P > 2 ? 2 : 0][i], y_s[P > 3 ? 3 : 0][i]};
+        const float y = ordered(q);
+        y_s[0][i] = l == 0.f ? 0.f : qs == qs ? y / l : qs;
+      }
+    }
+    __syncthreads();
   }
+  for (int i = threadIdx.x; i < nr * dt; i += 256) {
+    const int r = i / dt, c = i % dt * V, q_row = r0 + r;
+    if (d0 + c >= D) continue;
+    const int pos = a.by_G(q_row);
+    uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + pos) * (a.c.n_kv_heads * a.G) + h * a.G + (q_row - pos * a.G)) * D +
+                    d0 + c;
+    const float* y = &y_s[0][r * dims + c];
+    if (V == 1) {
+      dst[0] = f32_to_bf16(y[0]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(dst + v) = pack_bf16x2(y[v], y[v + 1 < V ? v + 1 : v]);
+    }
+  }
+}
+
+template <int P, int V, int U>
+cudaError_t launch_combine(const QAttnArgs& a, int rq, cudaStream_t st) {
+  const int dims = 256 / P / (a.rows < rq ? a.rows : rq) * V, runs = (a.c.dim + dims - 1) / dims;
+  const int64_t groups = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rq - 1) / rq);
+  return launch_k(qattn_combine_kernel<P, V, U>, dim3(static_cast<unsigned>(groups * runs)), dim3(256), 0, st, a, rq, runs);
 }
 
 template <int D, int RP>
@@ -970,13 +1015,12 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   if (a.n_splits == 1) return cudaSuccess;     // the results are out
-  // long lists of splits: fewer dims and more splits in flight in a thread (128
-  // splits of 36 rows: TUNED)
   const int rq = rp / 4;
+  if (a.n_splits <= 4) return launch_combine<1, 8, 4>(a, rq, st);
+  if (a.n_splits <= 8) return launch_combine<1, 4, 8>(a, rq, st);
   const int64_t groups = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rq - 1) / rq);
-  if (a.n_splits > 40)
-    return launch_k(qattn_combine_kernel<1, 32>, dim3(static_cast<unsigned>(groups * (D / 16))), dim3(256), 0, st, a, rq);
-  return launch_k(qattn_combine_kernel<4, 8>, dim3(static_cast<unsigned>(groups * (D / 64))), dim3(256), 0, st, a, rq);
+  if (a.n_splits > 40 && groups * D / 4 <= 4 * sms * rq) return launch_combine<4, 1, 32>(a, rq, st);
+  return launch_combine<4, 4, 8>(a, rq, st);
 }
 
 }  // namespace sv
