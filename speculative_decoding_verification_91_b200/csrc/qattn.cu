@@ -71,6 +71,21 @@ constexpr float kUnit = 32.f;
 constexpr float kLow = 16.f;               // w1 is stored times 16
 constexpr float kNoKey = -1e30f;           // reference of a row that has seen no key
 
+// Waits for this thread's loads from TMEM, v's among them.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));   // no use of v before
+}
+// 16 TMEM lanes by 32 columns: v[4 k + 2 i + z] is lane (thread / 4 + 8 i), column
+// 8 k + 2 (thread % 4) + z
+__device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+               : "r"(taddr));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -235,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   Item* items = reinterpret_cast<Item*>(tail + 512);       // [kItems]
   float* red = reinterpret_cast<float*>(tail + 1024);      // [threads of a row][rows]
   float* alpha_s = red + 256;                              // [rows]
+  float* l_s = alpha_s + 64;                               // [threads of a row][rows]: sums of p
+  float* bad_s = l_s + 256;                                // [rows]
   float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [kItems][kMaxScales]
   float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -535,13 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     const int row = rh * 32 + lane;
     const int st = (warp - kFirstSoft) * 32 + lane;               // 0..255
     // Rows of P and of the output: row r in quadrant r / RQ, lane r % RQ for w0,
-    // 16 + r % RQ for w1.  This thread's output row:
+    // RQ + r % RQ for w1.  The row of this thread's lane:
     constexpr int RQ = RP / 4;
-    const int o_idx = lane & 15, o_row = quad * RQ + o_idx;
+    const int o_row = quad * RQ + lane % RQ;
     const int p_row = (row / RQ) * 32 + row % RQ;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     constexpr int kSoft = kSoftWarps * 32;
     const int lg_bt = 31 - __clz(a.c.block);
+    float* l_r = l_s + rh * 32;
     float* red_r = red + rh * 32;              // [thread of the row][RP rows]
     int g = 0, p = 0;
     float qs = 0.f;
@@ -588,125 +606,219 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       __syncwarp();
       return true;
     };
-    // (all warps stop together, also after a timeout that only some have seen)
     bool have_item = take(0);
-    for (int item = 0; !bar_red_or(2, kSoft, !have_item); ++item) {
+    int item = 0;
+    float l_was = 0.f, m_was = 0.f;                   // of the item before
+    bool bad_was = false;
+    // Ends the item before: (m, l) and o = (o0 + o1 / 16) / kUnit.  Loads of 16
+    // lanes leave w0's and w1's sums of a row and a column in one thread (rows lane
+    // / 4 and 8 more, two columns of 8).
+    auto finish = [&]() {
+      const Item& x = items[(item - 1) % kItems];
+      wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      l_r[grp * RP + lane] = l_was;
+      if (grp == 0) bad_s[row] = bad_was ? 1.f : 0.f;
+      named_bar(1, kSoft);
+      tc_fence_after();
+      if (grp == 0 && row < x.nrows && a.n_splits > 1 && !*fail) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < NG; ++e) sum += l_r[e * RP + lane];
+        __stcg(&a.part_ml[x.slot + row], make_float2(m_was, sum));
+      }
+      if (quad * RQ < x.nrows) {
+        constexpr int NR = RQ / 8;                    // rows of a thread
+        float* po[NR];
+        uint16_t* dst[NR];
+        float sum[NR];
+        bool have[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = quad * RQ + lane / 4 + 8 * i;
+          have[i] = r < x.nrows && !*fail;
+          po[i] = a.part_o + (x.slot + r) * D + lane % 4 * 2;
+          if (a.n_splits == 1) {
+            const int pos = a.by_G(x.r0 + r);
+            dst[i] = a.out + ((x.out0 + pos) * (a.c.n_kv_heads * a.G) + x.h * a.G + (x.r0 + r - pos * a.G)) * D + lane % 4 * 2;
+            sum[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < NG; ++e) sum[i] += l_s[e * RP + r];
+            if (bad_s[r] != 0.f) sum[i] = __int_as_float(0x7fffffff);    // a NaN query
+          }
+        }
+        // 32 columns at a time, the next ones asked for before these are stored
+        auto readout = [&](auto direct) {
+          const int c_first = cg * (D / 2), c_end = c_first + D / 2;
+          uint32_t o[NR][16];
+          auto load = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) tmem_ld16x256(t_lane + (static_cast<uint32_t>(16 * i) << 16) + c0, o[i]);
+          };
+#pragma unroll 1
+          for (int c0 = c_first; c0 < c_end; c0 += 32) {
+            float2 y[NR][4];
+            load(c0);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) tmem_ld_wait_for(o[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < NR; ++i) {
+                const int e0 = 4 * k + 2 * i, e1 = NR == 2 ? e0 : 4 * k + 2;
+                y[i][k].x = fmaf(__uint_as_float(o[NR - 1][e1]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0]) * (1.f / kUnit));
+                y[i][k].y = fmaf(__uint_as_float(o[NR - 1][e1 + 1]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0 + 1]) * (1.f / kUnit));
+              }
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+              if (have[i]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if constexpr (decltype(direct)::value)
+                    *reinterpret_cast<uint32_t*>(dst[i] + c0 + 8 * k) =
+                        sum[i] == 0.f ? 0u : pack_bf16x2(y[i][k].x / sum[i], y[i][k].y / sum[i]);
+                  else
+                    __stcg(reinterpret_cast<float2*>(po[i] + c0 + 8 * k), y[i][k]);
+              }
+            __syncwarp();
+          }
+        };
+        if (a.n_splits == 1)
+          readout(std::true_type{});
+        else
+          readout(std::false_type{});
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_free);
+        mbar_arrive(&it_empty[(item - 1) % kItems]);
+      }
+    };
+    // An item is ended between the weights of the next one's first block and their
+    // store, which hides the wait for its last P V (one pass more ends the last).
+    // All warps stop together, also after a timeout that only some have seen.
+    for (;; ++item) {
+      const bool more = !bar_red_or(2, kSoft, !have_item);
+      if (!more && item == 0) break;
       const Item& x = items[item % kItems];
-      const int nrows = x.nrows, x_lo = x.lo, x_hi = x.hi, blk0 = x.blk0, nb = x.nb;
-      const long slot = x.slot;
+      const int nrows = more ? x.nrows : 0, x_lo = x.lo, x_hi = x.hi, blk0 = x.blk0, nb = more ? x.nb : 1;
       const bool half_used = rh * 32 < nrows;         // these warps hold rows
       const bool mine = row < nrows;
       const int row_lo = max(x_lo, a.window > 0 ? p - a.window + 1 : 0), row_hi = min(x_hi, p);
       const float* ks = ks_s + (item % kItems) * kMaxScales;
       const float* vs = vs_s + (item % kItems) * kMaxScales;
-      wait(&sc_full[item % kItems], (item / kItems) & 1);
+      if (more) wait(&sc_full[item % kItems], (item / kItems) & 1);
       float mref = kNoKey, l = 0.f;
       for (int j = 0; j < nb; ++j, ++g) {
         const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;
         constexpr int NE = KW / 16;                   // scales of the keys (one or two of 16-token blocks)
         float s[KW], f[NE], vsc[NE], cand = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < NE; ++u) {
-          const int e = ((j << kLgBlk) + grp * KW + 16 * u) >> lg_bt;
-          vsc[u] = vs[e];
-          f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), 3e38f);
-        }
-        wait(&s_full[g % SB], (g / SB) & 1);
-        __syncwarp();
-        tc_fence_after();
-        if (half_used) {
-          const uint32_t t_s = t_lane + C::kColS + (g % SB) * kBlk + grp * KW;
-#pragma unroll
-          for (int c = 0; c < KW; c += 8) tmem_ld8_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[8]>(&s[c]));
-          tmem_ld_wait();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[g % SB]);
-        if (half_used) {
-          bool edge = key0 < row_lo || key0 + KW - 1 > row_hi;
-#pragma unroll
-          for (int u = 0; u < NE; ++u) edge |= vsc[u] < 0.f;
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < KW; ++c)
-              if (key0 + c < row_lo || key0 + c > row_hi || vsc[c >> 4] < 0.f) s[c] = -INFINITY;
-          }
+        uint32_t w0[KW / 4], w1[KW / 4];
+        if (more) {
 #pragma unroll
           for (int u = 0; u < NE; ++u) {
-            float m4[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(fmaxf(s[16 * u + c], s[16 * u + 4 + c]), fmaxf(s[16 * u + 8 + c], s[16 * u + 12 + c]));
-            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            // log2 of the scale, rounded up to a whole number, within the range the sums can take
-            const uint32_t ub = __float_as_uint(vsc[u]);
-            int lv = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7fffffu) ? 1 : 0);
-            lv = vsc[u] < 0.f ? 0 : max(-100, min(100, lv));
-            cand = fmaxf(cand, fmaf(mx, f[u], static_cast<float>(lv)));
+            const int e = ((j << kLgBlk) + grp * KW + 16 * u) >> lg_bt;
+            vsc[u] = vs[e];
+            f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), 3e38f);
           }
+          wait(&s_full[g % SB], (g / SB) & 1);
           __syncwarp();
-        }
-        if (bar_red_or(1, kSoft, mine && cand > mref + kLazy)) {
-          red_r[grp * RP + lane] = cand;
-          named_bar(1, kSoft);
-          float bm = red_r[lane];
+          tc_fence_after();
+          if (half_used) {
+            const uint32_t t_s = t_lane + C::kColS + (g % SB) * kBlk + grp * KW;
 #pragma unroll
-          for (int e = 1; e < NG; ++e) bm = fmaxf(bm, red_r[e * RP + lane]);
-          float al = 1.f;
-          if (mine && bm > mref + kLazy) {
-            al = ex2(mref - bm);              // 0 while the row had no key
-            mref = bm;
-            l *= al;
+            for (int c = 0; c < KW; c += 8) tmem_ld8_nowait(t_s + c, *reinterpret_cast<uint32_t(*)[8]>(&s[c]));
+            tmem_ld_wait();
           }
-          if (j > 0) {
-            // the running sums of the rows that moved (all earlier P V done)
-            if (grp == 0) alpha_s[row] = al;
-            wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[g % SB]);
+          if (half_used) {
+            bool edge = key0 < row_lo || key0 + KW - 1 > row_hi;
+#pragma unroll
+            for (int u = 0; u < NE; ++u) edge |= vsc[u] < 0.f;
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < KW; ++c)
+                if (key0 + c < row_lo || key0 + c > row_hi || vsc[c >> 4] < 0.f) s[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int u = 0; u < NE; ++u) {
+              float m4[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) m4[c] = fmaxf(fmaxf(s[16 * u + c], s[16 * u + 4 + c]), fmaxf(s[16 * u + 8 + c], s[16 * u + 12 + c]));
+              const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+              // log2 of the scale, rounded up to a whole number, within the range the sums can take
+              const uint32_t ub = __float_as_uint(vsc[u]);
+              int lv = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7fffffu) ? 1 : 0);
+              lv = vsc[u] < 0.f ? 0 : max(-100, min(100, lv));
+              cand = fmaxf(cand, fmaf(mx, f[u], static_cast<float>(lv)));
+            }
+            __syncwarp();
+          }
+          if (bar_red_or(1, kSoft, mine && cand > mref + kLazy)) {
+            red_r[grp * RP + lane] = cand;
             named_bar(1, kSoft);
-            tc_fence_after();
-            al = o_row < nrows && o_idx < RQ ? alpha_s[o_row] : 1.f;
-            if (__any_sync(0xffffffffu, al != 1.f)) {
+            float bm = red_r[lane];
+#pragma unroll
+            for (int e = 1; e < NG; ++e) bm = fmaxf(bm, red_r[e * RP + lane]);
+            float al = 1.f;
+            if (mine && bm > mref + kLazy) {
+              al = ex2(mref - bm);              // 0 while the row had no key
+              mref = bm;
+              l *= al;
+            }
+            if (j > 0) {
+              // the running sums of the rows that moved (all earlier P V done)
+              if (grp == 0) alpha_s[row] = al;
+              wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+              named_bar(1, kSoft);
+              tc_fence_after();
+              al = o_row < nrows ? alpha_s[o_row] : 1.f;
+              if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 1
-              for (int c = cg * (D / 2); c < (cg + 1) * (D / 2); c += 32) {
-                uint32_t r8[4][8];
+                for (int c = cg * (D / 2); c < (cg + 1) * (D / 2); c += 32) {
+                  uint32_t r8[4][8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tmem_ld8_nowait(t_lane + c + 8 * e, r8[e]);
-                tmem_ld_wait();
+                  for (int e = 0; e < 4; ++e) tmem_ld8_nowait(t_lane + c + 8 * e, r8[e]);
+                  tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                  for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                  for (int z = 0; z < 8; ++z) r8[e][z] = __float_as_uint(__uint_as_float(r8[e][z]) * al);
-                  tmem_st8(t_lane + c + 8 * e, r8[e]);
+                    for (int z = 0; z < 8; ++z) r8[e][z] = __float_as_uint(__uint_as_float(r8[e][z]) * al);
+                    tmem_st8(t_lane + c + 8 * e, r8[e]);
+                  }
                 }
+                tmem_st_wait();
               }
-              tmem_st_wait();
             }
           }
-        }
-        uint32_t w0[KW / 4], w1[KW / 4];
-        if (half_used) {
+          if (half_used) {
 #pragma unroll
-          for (int c = 0; c < KW; c += 2) {
-            const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
-            const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
-            l += p0;
-            l += p1;
-            const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
-            uint16_t c0, c1;
-            uint32_t back;
-            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c0));
-            const __half2 rest = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLow));
-            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
-            if ((c & 2) == 0) {
-              w0[c >> 2] = c0;
-              w1[c >> 2] = c1;
-            } else {
-              w0[c >> 2] |= static_cast<uint32_t>(c0) << 16;
-              w1[c >> 2] |= static_cast<uint32_t>(c1) << 16;
+            for (int c = 0; c < KW; c += 2) {
+              const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
+              const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
+              l += p0;
+              l += p1;
+              const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
+              uint16_t c0, c1;
+              uint32_t back;
+              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c0));
+              const __half2 rest = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLow));
+              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+              if ((c & 2) == 0) {
+                w0[c >> 2] = c0;
+                w1[c >> 2] = c1;
+              } else {
+                w0[c >> 2] |= static_cast<uint32_t>(c0) << 16;
+                w1[c >> 2] |= static_cast<uint32_t>(c1) << 16;
+              }
             }
           }
         }
+        if (j == 0 && item > 0) finish();
+        if (!more) break;
         // the P buffer was last read by P V of block g - PB
         if (g >= PB) wait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1);
         if (mine) {
@@ -715,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           for (int u = 0; u < NE; ++u) {
             *reinterpret_cast<uint4*>(pp + swz128(p_row, NE * grp + u)) =
                 make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
-            *reinterpret_cast<uint4*>(pp + swz128(p_row + 16, NE * grp + u)) =
+            *reinterpret_cast<uint4*>(pp + swz128(p_row + RQ, NE * grp + u)) =
                 make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
           }
         }
@@ -738,75 +850,11 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
-      // ---- this item's l, the next item's queries, then (m, l) and o = (o0 + o1
-      // / 16) / kUnit, lanes 16 apart adding two columns at a time
-      const int nr = min(RQ, nrows - quad * RQ);      // output rows of this quadrant
-      float* po = a.part_o + (slot + quad * RQ) * D + o_idx;
-      const long out_at = a.n_splits == 1 ? x.out0 + (x.r0 + o_row) / a.G : 0;
-      const int out_h = a.n_splits == 1 ? x.h * a.G + (x.r0 + o_row) % a.G : 0;
-      const bool bad = bad_q;
+      if (!more) break;
+      l_was = l;
+      m_was = mref;
+      bad_was = bad_q;
       have_item = take(item + 1);
-      wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-      // (every warp is past the last block's reductions)
-      red_r[grp * RP + lane] = l;
-      if (grp == 0) alpha_s[row] = bad ? 1.f : 0.f;
-      named_bar(1, kSoft);
-      tc_fence_after();
-      if (grp == 0 && mine && a.n_splits > 1 && !*fail) {
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < NG; ++e) sum += red_r[e * RP + lane];
-        __stcg(&a.part_ml[slot + row], make_float2(mref, sum));
-      }
-      if (nr > 0) {
-        const bool low = lane >= 16, store = o_idx < nr && !*fail;
-        const float f_own = low ? 1.f / (kUnit * kLow) : 1.f / kUnit, f_got = low ? 1.f / kUnit : 1.f / (kUnit * kLow);
-        float sum = 0.f;
-        uint16_t* dst = nullptr;
-        if (a.n_splits == 1 && store) {
-          dst = a.out + (out_at * (a.c.n_kv_heads * a.G) + out_h) * D;
-#pragma unroll
-          for (int e = 0; e < NG; ++e) sum += red[e * RP + o_row];
-          if (alpha_s[o_row] != 0.f) sum = __int_as_float(0x7fffffff);    // a NaN query
-        }
-        // the lanes of w0's sums finish the columns at 0, step, .. and those of w1's
-        // the ones at off, off + step, .. of 32
-        auto finish = [&](auto step_, auto off_, auto&& out) {
-          constexpr int step = decltype(step_)::value, off = decltype(off_)::value;
-#pragma unroll 1
-          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += 32) {
-            float o[32], y[16];
-            tmem_ld32(t_lane + c0, o);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float got = __shfl_xor_sync(0xffffffffu, low ? o[step * c] : o[step * c + off], 16);
-              y[c] = fmaf(got, f_got, (low ? o[step * c + off] : o[step * c]) * f_own);
-            }
-            if (store) out(c0 + (low ? off : 0), y);
-          }
-        };
-        if (a.n_splits > 1) {     // [dim][row]: two whole dims a store
-          finish(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{}, [&](int c0, const float(&y)[16]) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) __stcg(po + (c0 + 2 * c) * nr, y[c]);
-          });
-        } else {                  // the row's result: 16 dims next to each other
-          finish(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{}, [&](int c0, const float(&y)[16]) {
-            uint32_t v[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = sum == 0.f ? 0u : pack_bf16x2(y[2 * c] / sum, y[2 * c + 1] / sum);
-            uint4* d = reinterpret_cast<uint4*>(dst + c0);
-            d[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            d[1] = make_uint4(v[4], v[5], v[6], v[7]);
-          });
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(o_free);
-        mbar_arrive(&it_empty[item % kItems]);
-      }
     }
   }
   tc_fence_before();
@@ -815,76 +863,86 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row.
-// The partials of the rq <= 16 rows of a group (a lane quadrant of the split
-// kernel) lie [dim][row], and a thread takes V of a run of dims for one row.  Four
-// sums are kept by split index mod 4, each in ascending order, and added in the
-// order of the absolute index: by one thread (P = 1) or by four (P = 4), which
-// changes no bit, nor do V and U.  Splits without a key of the row add nothing at
-// fixed places, so the order does not depend on where the list of splits starts.
-// The time is a chain of memory latencies: the sequence's length, the references
-// and the first P U splits' partials are all asked for at once, those beyond the
-// sequence's last split (whatever the workspace holds) are dropped.
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits of a row, V
+// dims a thread.  Four sums are kept by split index mod 4, each in ascending order,
+// and added in the order of the absolute index: by one thread (P = 1) or by four
+// (P = 4), which changes no bit, nor do V and U.  Splits without a key of the row
+// add nothing at fixed places, so the order does not depend on where the list of
+// splits starts.  The time is a chain of memory latencies: the sequence's length,
+// the references and the first P U splits' partials are all asked for at once,
+// those beyond the sequence's last split (whatever the workspace holds) are dropped.
 template <int P, int V, int U>
-__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a, int rq, int runs) {
+__global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constant__ QAttnArgs a) {
   constexpr int NT = 256 / P, NA = 4 / P;
-  constexpr int kTile = P * U < 16 ? 16 : P * U;   // splits whose weights are held at a time
-  __shared__ float w_s[kTile][16], l_s[kTile][16], m_s[16][16];
-  __shared__ float y_s[P][16 + NT * V], d_s[P][16];
+  constexpr int kTile = P * U < 32 ? 32 : P * U;   // splits whose weights are held at a time
+  constexpr int kRows = NT * V / 128 < 1 ? 1 : NT * V / 128;
+  __shared__ float w_s[kRows][kTile], l_s[kRows][kTile], m_s[8], d_s[P > 1 ? P : 1][P > 1 ? NT : 1];
+  __shared__ int n_s[8];
+  __shared__ float y_s[P > 1 ? P : 1][P > 1 ? NT * V : 1];
   pdl_trigger();
   pdl_wait();
-  const int D = a.c.dim, groups = (a.rows + rq - 1) / rq;
-  const int run = blockIdx.x % runs, bhg = blockIdx.x / runs, grp = bhg % groups, bh = bhg / groups;
-  const int h = bh % a.c.n_kv_heads, b = bh / a.c.n_kv_heads;
-  const int r0 = grp * rq, nr = min(rq, a.rows - r0);
-  const int dt = NT / nr, dims = dt * V, d0 = run * dims;    // dims next to each other in threads; of the run
-  if (d0 >= D) return;                                       // (groups of few rows need fewer runs)
-  const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r0;
+  const int D = a.c.dim, lr = min(D / V, NT), lg = 31 - __clz(lr);   // threads of a row and sum
+  const int p = threadIdx.x / NT, el = threadIdx.x % NT, rr = el >> lg;
+  const int me = p * lr + (el & (lr - 1)), all = P * lr;             // among the row's threads
+  const int64_t flat = (static_cast<int64_t>(blockIdx.x) * NT + el) * V;
+  const int at = static_cast<int>(flat >> (D == 256 ? 8 : 7)), c = static_cast<int>(flat) & (D - 1);
+  const bool have = at < a.B * a.c.n_kv_heads * a.rows;
+  const int bh = have ? at / a.rows : 0, r = have ? at - bh * a.rows : 0, b = bh / a.c.n_kv_heads, h = bh - b * a.c.n_kv_heads;
+  const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r;
   const int L = a.c.seq_lens[b];
-  const int p = threadIdx.x / NT, el = threadIdx.x % NT, row = el % nr, td = el / nr;
-  const bool mine = td < dt;
-  const int trow = threadIdx.x & 15, ts = threadIdx.x >> 4;  // of the references: row, split
-  const float* po = a.part_o + slot0 * D + p * static_cast<int64_t>(a.rows) * D + (d0 + td) * nr + row;
   const int64_t step = static_cast<int64_t>(a.rows) * D;
-  bool want[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) want[v] = mine && d0 + td + dt * v < D;
+  const float* po = a.part_o + slot0 * D + p * step + c;
   float x[U][V];
   auto load = [&](int s0) {
-    const float* at = po + s0 * step;
+    const float* at_s = po + s0 * step;
 #pragma unroll
-    for (int u = 0; u < U; ++u, at += P * step)
+    for (int u = 0; u < U; ++u, at_s += P * step) {
+      if (have && s0 + P * u + p < a.n_splits) {
+        if (V == 4) {
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(at_s));
+          x[u][0] = z.x;
+          x[u][V > 1 ? 1 : 0] = z.y;
+          x[u][V > 2 ? 2 : 0] = z.z;
+          x[u][V > 3 ? 3 : 0] = z.w;
+        } else {
+          x[u][0] = __ldcg(at_s);
+        }
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        x[u][v] = want[v] && s0 + P * u + p < a.n_splits ? __ldcg(at + dt * v * nr) : 0.f;
+        for (int v = 0; v < V; ++v) x[u][v] = 0.f;
+      }
+    }
   };
   auto load_tile = [&](int s0) {                   // references into w_s, sums into l_s
-    float2 ml[kTile / 16];
-#pragma unroll
-    for (int i = 0; i < kTile / 16; ++i) {
-      const int s = s0 + i * 16 + ts;
-      ml[i] = trow < nr && s < a.n_splits ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s) * a.rows + trow])
-                                          : make_float2(kNoKey, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < kTile / 16; ++i) {
-      w_s[i * 16 + ts][trow] = ml[i].x;
-      l_s[i * 16 + ts][trow] = ml[i].y;
+    for (int s = me; s < kTile; s += all) {
+      const float2 ml = have && s0 + s < a.n_splits ? __ldcg(&a.part_ml[slot0 + static_cast<int64_t>(s0 + s) * a.rows])
+                                                    : make_float2(kNoKey, 0.f);
+      w_s[rr][s] = ml.x;
+      l_s[rr][s] = ml.y;
     }
   };
   load(0);
-  const float qs = __ldcg(&a.q_scale[static_cast<int64_t>(bh) * a.rows + r0 + row]);
+  const float qs = have ? __ldcg(&a.q_scale[at]) : 0.f;
   load_tile(0);
   const SeqKeys k = seq_keys(a, L);
   float M = kNoKey;
   for (int s0 = 0; s0 < k.splits; s0 += kTile) {
     if (s0 > 0) load_tile(s0);                     // each thread reads back what it wrote
-    for (int s = ts; s < min(kTile, k.splits - s0); s += 16) M = fmaxf(M, w_s[s][trow]);
+    for (int s = me; s < min(kTile, k.splits - s0); s += all) M = fmaxf(M, w_s[rr][s]);
   }
-  m_s[ts][trow] = M;
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) M = fmaxf(M, m_s[i][trow]);
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    m_s[warp] = M;
+    n_s[warp] = k.splits;
+  }
+  __syncthreads();
+  // (a row's threads are whole warps: lr / 32 next to each other for each sum)
+  const int wr = lr >> 5, w0 = rr * wr;
+#pragma unroll
+  for (int q = 0; q < P; ++q)
+    for (int i = 0; i < wr; ++i) M = fmaxf(M, m_s[q * (NT / 32) + w0 + i]);
   float acc[NA][V], den[NA];
 #pragma unroll
   for (int q = 0; q < NA; ++q) {
@@ -892,15 +950,18 @@ __global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constan
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[q][v] = 0.f;
   }
-  for (int s0 = 0; s0 < k.splits; s0 += kTile) {
+  int most = k.splits;                             // of the CTA's rows
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, n_s[i]);
+  for (int s0 = 0; s0 < most; s0 += kTile) {
     const int ns = min(kTile, k.splits - s0);
-    if (k.splits > kTile) {
+    if (most > kTile) {
       __syncthreads();
       load_tile(s0);
     }
-    for (int s = ts; s < ns; s += 16) {
-      const float m = w_s[s][trow];
-      w_s[s][trow] = m <= kNoKey ? 0.f : exp2f(m - M);
+    for (int s = me; s < ns; s += all) {
+      const float m = w_s[rr][s];
+      w_s[rr][s] = m <= kNoKey ? 0.f : exp2f(m - M);
     }
     __syncthreads();
     for (int u0 = 0; u0 < ns; u0 += P * U) {
@@ -908,9 +969,9 @@ __global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constan
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int s = u0 + P * u + p;
-        const float w = s < ns ? w_s[s][row] : 0.f;
+        const float w = s < ns ? w_s[rr][s] : 0.f;
         if (w > 0.f) {                             // (a split without keys of the row has no sums)
-          den[u % NA] = fmaf(w, l_s[s][row], den[u % NA]);
+          den[u % NA] = fmaf(w, l_s[rr][s], den[u % NA]);
 #pragma unroll
           for (int v = 0; v < V; ++v) acc[u % NA][v] = fmaf(w, x[u][v], acc[u % NA][v]);
         }
@@ -919,66 +980,46 @@ __global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constan
   }
   // the four sums in the order of the absolute split index
   const int turn = k.splits ? a.by_split(k.lo / kBlk) & 3 : 0;
-  auto ordered = [&](const float(&q)[4]) {
-    float z[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      z[i] = turn == 0 ? q[i] : turn == 1 ? q[(i + 3) & 3] : turn == 2 ? q[(i + 2) & 3] : q[(i + 1) & 3];
-    return ((z[0] + z[1]) + z[2]) + z[3];
+  auto ordered = [&](float q0, float q1, float q2, float q3) {
+    const float z0 = turn == 0 ? q0 : turn == 1 ? q3 : turn == 2 ? q2 : q1;
+    const float z1 = turn == 0 ? q1 : turn == 1 ? q0 : turn == 2 ? q3 : q2;
+    const float z2 = turn == 0 ? q2 : turn == 1 ? q1 : turn == 2 ? q0 : q3;
+    const float z3 = turn == 0 ? q3 : turn == 1 ? q2 : turn == 2 ? q1 : q0;
+    return ((z0 + z1) + z2) + z3;
   };
-  // [row][dim] of the run, each row's dims next to each other
+  float y[V], l;
   if (P == 1) {
-    if (mine) {
-      const float l = ordered(reinterpret_cast<const float(&)[4]>(den));
+    l = ordered(den[0], den[1 % NA], den[2 % NA], den[3 % NA]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float q[4] = {acc[0][v], acc[NA > 1 ? 1 : 0][v], acc[NA > 2 ? 2 : 0][v], acc[NA > 3 ? 3 : 0][v]};
-        const float y = ordered(q);
-        y_s[0][row * dims + td + dt * v] = l == 0.f ? 0.f : qs == qs ? y / l : qs;   // no key: zero
-      }
-    }
-    __syncthreads();
+    for (int v = 0; v < V; ++v) y[v] = ordered(acc[0][v], acc[1 % NA][v], acc[2 % NA][v], acc[3 % NA][v]);
   } else {
-    if (mine) {
-      if (td == 0) d_s[p][row] = den[0];
+    d_s[p][el] = den[0];
 #pragma unroll
-      for (int v = 0; v < V; ++v) y_s[p][row * dims + td + dt * v] = acc[0][v];
-    }
+    for (int v = 0; v < V; ++v) y_s[p][v * NT + el] = acc[0][v];
     __syncthreads();
-    if (p == 0 && mine) {
-      const float dq[4] = {d_s[0][row], d_s[P > 1 ? 1 : 0][row], d_s[P > 2 ? 2 : 0][row], d_s[P > 3 ? 3 : 0][row]};
-      const float l = ordered(dq);
+    if (p > 0) return;
+    l = ordered(d_s[0][el], d_s[1 % P][el], d_s[2 % P][el], d_s[3 % P][el]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int i = row * dims + td + dt * v;
-        const float q[4] = {y_s[0][i], y_s[P > 1 ? 1 : 0][i], y_s[P > 2 ? 2 : 0][i], y_s[P > 3 ? 3 : 0][i]};
-        const float y = ordered(q);
-        y_s[0][i] = l == 0.f ? 0.f : qs == qs ? y / l : qs;
-      }
-    }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < nr * dt; i += 256) {
-    const int r = i / dt, c = i % dt * V, q_row = r0 + r;
-    if (d0 + c >= D) continue;
-    const int pos = a.by_G(q_row);
-    uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + pos) * (a.c.n_kv_heads * a.G) + h * a.G + (q_row - pos * a.G)) * D +
-                    d0 + c;
-    const float* y = &y_s[0][r * dims + c];
-    if (V == 1) {
-      dst[0] = f32_to_bf16(y[0]);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(dst + v) = pack_bf16x2(y[v], y[v + 1 < V ? v + 1 : v]);
+    for (int v = 0; v < V; ++v) {
+      const int i = v * NT + el;
+      y[v] = ordered(y_s[0][i], y_s[1 % P][i], y_s[2 % P][i], y_s[3 % P][i]);
     }
   }
+  if (!have) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) y[v] = l == 0.f ? 0.f : qs == qs ? y[v] / l : qs;     // no key: zero
+  const int pos = a.by_G(r);
+  uint16_t* dst = a.out + ((static_cast<int64_t>(b) * a.n + pos) * (a.c.n_kv_heads * a.G) + h * a.G + (r - pos * a.G)) * D + c;
+  if (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y[0], y[1 % V]), pack_bf16x2(y[2 % V], y[3 % V]));
+  else
+    *dst = f32_to_bf16(y[0]);
 }
 
 template <int P, int V, int U>
-cudaError_t launch_combine(const QAttnArgs& a, int rq, cudaStream_t st) {
-  const int dims = 256 / P / (a.rows < rq ? a.rows : rq) * V, runs = (a.c.dim + dims - 1) / dims;
-  const int64_t groups = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rq - 1) / rq);
-  return launch_k(qattn_combine_kernel<P, V, U>, dim3(static_cast<unsigned>(groups * runs)), dim3(256), 0, st, a, rq, runs);
+cudaError_t launch_combine(const QAttnArgs& a, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.c.n_kv_heads * a.rows, per = 256 / P * V;
+  return launch_k(qattn_combine_kernel<P, V, U>, dim3(static_cast<unsigned>((rows * a.c.dim + per - 1) / per)), dim3(256), 0, st, a);
 }
 
 template <int D, int RP>
@@ -1015,12 +1056,11 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   if (a.n_splits == 1) return cudaSuccess;     // the results are out
-  const int rq = rp / 4;
-  if (a.n_splits <= 4) return launch_combine<1, 8, 4>(a, rq, st);
-  if (a.n_splits <= 8) return launch_combine<1, 4, 8>(a, rq, st);
-  const int64_t groups = static_cast<int64_t>(a.B) * a.c.n_kv_heads * ((a.rows + rq - 1) / rq);
-  if (a.n_splits > 40 && groups * D / 4 <= 4 * sms * rq) return launch_combine<4, 1, 32>(a, rq, st);
-  return launch_combine<4, 4, 8>(a, rq, st);
+  if (a.n_splits <= 4) return launch_combine<1, 4, 4>(a, st);
+  if (a.n_splits <= 8) return launch_combine<1, 4, 8>(a, st);
+  const int64_t all = static_cast<int64_t>(a.B) * a.c.n_kv_heads * a.rows;
+  if (a.n_splits > 40 && all * D <= 4 * sms * 64) return launch_combine<4, 1, 32>(a, st);
+  return launch_combine<4, 4, 8>(a, st);
 }
 
 }  // namespace sv
