@@ -60,9 +60,10 @@ constexpr int kFirstSoft = 4;
 constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
 constexpr uint32_t kSmemMax = 227u * 1024u;
 constexpr int kItems = 4;                  // items described ahead in shared memory
-constexpr uint32_t kTail = 12288;
+constexpr uint32_t kTail = 16384;
 constexpr uint32_t kPBytes = 128 * kBlk;
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
+constexpr int kMaxPg = 256;                // its pages: 16384 keys / 64
 // p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448.  A larger
 // kLazy moves the reference less often, a larger kUnit keeps smaller weights
 // (w1's least step is 2^-9 / (kUnit kLow) = 2^-18 of the reference).
@@ -141,7 +142,6 @@ struct Item {
   int fresh, pad;          // the queries differ from the item before
   long slot;               // partial of its first row
   long q_row;              // row of its first query among all
-  long page0;              // the sequence's block-table row
   long out0;               // row of the sequence's first result
 };
 
@@ -188,7 +188,7 @@ struct Walker {
           h = 0;
           do {
             if (++b >= a->B) return;
-            load_seq(a->c.seq_lens[b]);
+            load_seq(__ldcg(&a->c.seq_lens[b]));
           } while (k.blocks == 0);
         }
       }
@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   float* bad_s = l_s + 256;                                // [rows]
   float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [kItems][kMaxScales]
   float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
+  int* pg_s = reinterpret_cast<int*>(vs_s + kItems * kMaxScales);   // [kItems][kMaxPg]; < 0: not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(sizeof(Item) * kItems <= 512, "items");
 
@@ -286,8 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_trigger();
-  pdl_wait();
-
+  // Lengths, block table, pages and scales are read at once, the softmax warps
+  // alone wait for the query kernel: it lets this one start only once every kernel
+  // before it is done (it triggers after its own wait), so what it does not write
+  // itself is final, and nothing earlier still reads the partials.  (Those loads
+  // pass by L1, which nothing has ordered yet.)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -313,17 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           more = false;
           continue;
         }
-        const int32_t* bt = a.c.block_table + x.page0;
         int y[2];
         uint32_t bytes = 0;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const int pg = (x.blk0 + j) * 2 + p;
-          int id = -1;
-          if (pg * kPg <= x.hi && pg * kPg + kPg - 1 >= x.lo) id = bt[pg];
-          const bool there = id >= 0 && id < a.c.num_pages;
-          y[p] = there ? (id * a.c.n_kv_heads + x.h) * kPg : -1;
-          if (there) bytes += kPg * D;
+          const int id = pg_s[(i % kItems) * kMaxPg + j * 2 + p];
+          y[p] = id >= 0 ? (id * a.c.n_kv_heads + x.h) * kPg : -1;
+          if (id >= 0) bytes += kPg * D;
         }
         if (u >= NU && !(ok = wait(&u_empty[s], ((u / NU) - 1) & 1))) break;
         mbar_arrive_expect_tx(&u_full[s], bytes);
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     // --------------------------------------------------- items and scales
     const int RB = (a.rows + RP - 1) / RP, per_b = a.c.n_kv_heads * RB;
     // this CTA's share [x0, x1) of all key blocks and its first item
-    const auto length = [&](int b) { return b < a.B ? a.c.seq_lens[b] : 0; };
+    const auto length = [&](int b) { return b < a.B ? __ldcg(&a.c.seq_lens[b]) : 0; };
     const auto blocks = [&](int b, int L) { return b < a.B ? seq_keys(a, L).blocks * per_b : 0; };
     int L = length(lane), n = blocks(lane, L), total = 0;
     for (int b = lane; b - lane < a.B; b += 32) {
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         w.next();
       }
     }
-    const int per_page = kPg / a.c.block;
+    const int lg_bt = 31 - __clz(a.c.block), lg_pg = 31 - __clz(kPg);
     bool fresh = true;
     for (int i = 0;; w.next()) {
       const bool end = !w.valid();
@@ -511,27 +511,37 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         x.fresh = fresh;
         x.slot = slot;
         x.q_row = bh * a.rows + r0;
-        x.page0 = static_cast<long>(w.b) * a.c.max_pages;
         x.out0 = static_cast<long>(w.b) * a.n;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&it_full[q]);      // the copies may start; the scales follow
+      // its pages, all asked for at once (one at a time by the producer they cost an
+      // L2 latency a block), then its scales; the copies start before those are here
       if (!end) {
-        fresh = false;
         const int32_t* bt = a.c.block_table + static_cast<int64_t>(w.b) * a.c.max_pages;
-        const int count = w.nb * (kBlk / a.c.block);
-        for (int e = lane; e < count; e += 32) {
-          const int key = (w.blk0 << kLgBlk) + e * a.c.block, pg = key / kPg;
-          float ks = 0.f, vs = -1.f;
+        for (int e = lane; e < 2 * w.nb; e += 32) {
+          const int pg = 2 * w.blk0 + e;
+          int id = -1;
           if (pg * kPg <= w.hi && pg * kPg + kPg - 1 >= w.lo) {
-            const int id = bt[pg];
-            if (id >= 0 && id < a.c.num_pages) {
-              const int64_t sc = (static_cast<int64_t>(id) * a.c.n_kv_heads + w.h) * per_page + (key % kPg) / a.c.block;
-              ks = a.c.ks[sc];
-              vs = a.c.vs[sc];
-            } else {
+            id = __ldcg(&bt[pg]);
+            if (id < 0 || id >= a.c.num_pages) {
+              id = -1;
               flag_status(a.c.status, SPEC_DEV_BAD_PAGE);
             }
+          }
+          pg_s[q * kMaxPg + e] = id;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_full[q]);
+      if (!end) {
+        fresh = false;
+        const int count = w.nb * (kBlk / a.c.block), lg_per = lg_pg - lg_bt;
+        for (int e = lane; e < count; e += 32) {
+          const int id = pg_s[q * kMaxPg + (e >> lg_per)];
+          float ks = 0.f, vs = -1.f;
+          if (id >= 0) {
+            const int64_t sc = ((static_cast<int64_t>(id) * a.c.n_kv_heads + w.h) << lg_per) + (e & ((1 << lg_per) - 1));
+            ks = __ldcg(&a.c.ks[sc]);
+            vs = __ldcg(&a.c.vs[sc]);
           }
           ks_s[q * kMaxScales + e] = ks;
           vs_s[q * kMaxScales + e] = vs;
@@ -606,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       __syncwarp();
       return true;
     };
+    pdl_wait();
     bool have_item = take(0);
     int item = 0;
     float l_was = 0.f, m_was = 0.f;                   // of the item before
@@ -880,7 +891,6 @@ __global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constan
   __shared__ int n_s[8];
   __shared__ float y_s[P > 1 ? P : 1][P > 1 ? NT * V : 1];
   pdl_trigger();
-  pdl_wait();
   const int D = a.c.dim, lr = min(D / V, NT), lg = 31 - __clz(lr);   // threads of a row and sum
   const int p = threadIdx.x / NT, el = threadIdx.x % NT, rr = el >> lg;
   const int me = p * lr + (el & (lr - 1)), all = P * lr;             // among the row's threads
@@ -889,7 +899,8 @@ __global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constan
   const bool have = at < a.B * a.c.n_kv_heads * a.rows;
   const int bh = have ? at / a.rows : 0, r = have ? at - bh * a.rows : 0, b = bh / a.c.n_kv_heads, h = bh - b * a.c.n_kv_heads;
   const int64_t slot0 = static_cast<int64_t>(bh) * a.n_splits * a.rows + r;
-  const int L = a.c.seq_lens[b];
+  const int L = __ldcg(&a.c.seq_lens[b]);                   // (final: see the split kernel's start)
+  const SeqKeys k = seq_keys(a, L);
   const int64_t step = static_cast<int64_t>(a.rows) * D;
   const float* po = a.part_o + slot0 * D + p * step + c;
   float x[U][V];
@@ -921,10 +932,10 @@ __global__ void __launch_bounds__(256) qattn_combine_kernel(const __grid_constan
       l_s[rr][s] = ml.y;
     }
   };
+  pdl_wait();
   load(0);
   const float qs = have ? __ldcg(&a.q_scale[at]) : 0.f;
   load_tile(0);
-  const SeqKeys k = seq_keys(a, L);
   float M = kNoKey;
   for (int s0 = 0; s0 < k.splits; s0 += kTile) {
     if (s0 > 0) load_tile(s0);                     // each thread reads back what it wrote

@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
                                                            const __grid_constant__ QAttnArgs a) {
   constexpr int P = D / 32;
   __shared__ float2 cs[kMaxPairs];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();   // after the wait: what ran before is done when the split kernel starts
   const int H = a.c.n_kv_heads, n_heads = H * a.G, lane = threadIdx.x & 31;
   const int64_t bi = blockIdx.x;
   const int b = static_cast<int>(bi / a.n), i = static_cast<int>(bi % a.n);
