@@ -3,20 +3,24 @@
 //
 //   y0 = x0 c - x1 s,  y1 = x0 s + x1 c,   (c, s) = magnitude (cos, sin)(t f_j)
 //
-// Bound by memory: every element is read and written once.  A CTA takes `rows`
-// rows of `heads` heads; their cosines and sines are formed once in shared
-// memory, while the first loads are on their way (a thread's own angles for every
-// pair would be 30 instructions an element).  Two forms:
+// Bound by memory: every element is read and written once.  Angles are formed once
+// for a row and all heads (a thread's own for every pair would be 30 instructions an
+// element).  Two forms:
 //   direct  where 16-byte pieces hold whole pairs (interleaved) or lie opposite
-//           each other (half: span / 2 a multiple of the piece): a thread turns a
-//           piece, or two opposite ones, in registers.
+//           each other (half: span / 2 a multiple of the piece): a thread keeps a
+//           piece, or two opposite ones, of the head, forms their angles in
+//           registers while the piece's loads of several heads are on their way,
+//           turns them and goes on to its next row.  (Angles passed round a CTA in
+//           shared memory: 61 us for the case below.)
 //   staged  any other span or alignment: the heads pass through shared memory, in
 //           16-byte pieces where rows and heads are aligned to them, else element
 //           by element.
-// 32,768 rows of 8 x 256 bf16, interleaved: TUNED
+// 32,768 rows of 8 x 256 bf16, interleaved: 46.0 us, 5.8 TB/s (with 256 threads a CTA
+// 51.5; four loads in flight instead of eight 48.0).  5 x 16 x 256: 2.5 us in a graph.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -28,15 +32,17 @@ namespace sv {
 
 namespace {
 
-constexpr int kRopeOpThreads = 256;
+constexpr int kRopeOpThreads = 256;     // staged
+constexpr int kDirectThreads = 128;
 constexpr int kRopeRows = 32;           // rows of a CTA
 constexpr int kRopeTile = 16384;        // bytes of heads of a CTA
 
 struct RopePlan {
-  int rows, heads, head_blocks;   // of a CTA; CTAs across the heads
-  int units;                      // pieces (direct) of a head
-  int n_tab;                      // n_rot, to whole pieces (direct)
-  Div by_units, by_heads, by_pairs, by_n;   // by_n: pieces of a row
+  int rows, heads;                // direct: of a thread; staged: of a CTA
+  int units;                      // pieces (or elements) of a head
+  int groups, side, chunks;       // direct: of heads; rows side by side in a CTA; CTAs across a row's pieces
+  int head_blocks;                // staged: CTAs across the heads
+  Div by_units, by_heads, by_pairs, by_n;   // by_n: a row's pieces and groups
 };
 
 template <typename T>
@@ -60,7 +66,25 @@ template <typename T>
 union Piece {
   uint4 v;
   T e[16 / sizeof(T)];
+  uint32_t w[4];
 };
+
+// Two 16-bit elements of a word.
+template <typename T>
+__device__ __forceinline__ float2 two(uint32_t w) {
+  if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t word(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
 
 template <typename T>
 __device__ __forceinline__ void turn(T& a, T& b, float2 cs) {
@@ -69,10 +93,32 @@ __device__ __forceinline__ void turn(T& a, T& b, float2 cs) {
   b = from_f<T>(x0 * cs.y + x1 * cs.x);
 }
 
-// Positions and (c, s) of the CTA's rows; ends with a barrier.  PP pairs of a piece:
-// pair j of a row at [j % PP][j / PP], so that the lanes of a warp, a piece each, read
-// next to each other (in pair order the bank conflicts took half of the kernel's time).
-template <int PP>
+// A whole piece's pairs (HALF: with the opposite piece b).  16-bit elements two at a time: taken out and rounded one by
+// one they were a third of the kernel's instructions.
+template <typename T, bool HALF>
+__device__ __forceinline__ void turn_piece(Piece<T>& a, Piece<T>& b, const float2 (&c)[(HALF ? 16 : 8) / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = two<T>(a.w[e]);
+      if (HALF) {
+        const float2 y = two<T>(b.w[e]), c0 = c[HALF ? 2 * e : 0], c1 = c[HALF ? 2 * e + 1 : 0];
+        a.w[e] = word<T>(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+        b.w[e] = word<T>(x.x * c0.y + y.x * c0.x, x.y * c1.y + y.y * c1.x);
+      } else {
+        const float2 c0 = c[e];
+        a.w[e] = word<T>(x.x * c0.x - x.y * c0.y, x.x * c0.y + x.y * c0.x);
+      }
+    }
+  } else {
+    constexpr int E = 16 / sizeof(T);
+#pragma unroll
+    for (int e = 0; e < (HALF ? E : E / 2); ++e)
+      turn(a.e[HALF ? e : 2 * e], HALF ? b.e[e] : a.e[2 * e + 1], c[e]);
+  }
+}
+
+// Positions and (c, s) of the CTA's rows; ends with a barrier.
 __device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, const RopePlan& p, int64_t row0,
                                        float2* cs, int* pos) {
   const int n = p.rows * r.n_rot;
@@ -83,99 +129,80 @@ __device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, c
     const int at = row0 + t < a.n_rows ? a.positions[row0 + t] : -1;
     float c = 1.f, s = 0.f;
     if (at >= 0) rope_turn(at, r.step[j], static_cast<float>(r.magnitude), c, s);
-    cs[t * p.n_tab + (PP == 1 ? j : j % PP * (p.n_tab / PP) + j / PP)] = make_float2(c, a.inverse ? -s : s);
+    cs[i] = make_float2(c, a.inverse ? -s : s);
   }
   __syncthreads();
 }
 
-// A thread keeps its piece (or two opposite ones) of a head and goes down the CTA's
-// rows, so that what depends on the piece is formed once.
+// A thread keeps its piece (or two opposite ones) of a head, and with it the pairs'
+// frequencies, and goes down the CTA's rows.
 template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kRopeOpThreads) rope_direct_kernel(const __grid_constant__ RopeArgs r,
+__global__ void __launch_bounds__(kDirectThreads) rope_direct_kernel(const __grid_constant__ RopeArgs r,
                                                                      const __grid_constant__ RopeOpArgs a,
                                                                      const __grid_constant__ RopePlan p) {
   constexpr int E = 16 / sizeof(T);
   constexpr bool HALF = LAYOUT == SPEC_ROPE_HALF;
-  constexpr int B = HALF ? 2 : 4;          // rows in flight of a thread: four 16-byte loads
+  constexpr int B = HALF ? 4 : 8;          // heads in flight of a thread: eight 16-byte loads
   constexpr int PP = HALF ? E : E / 2;     // pairs of a piece
-  extern __shared__ float2 cs[];
-  __shared__ int pos[kRopeRows];
   pdl_trigger();
   pdl_wait();
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.head_blocks) * p.rows;
-  const int h0 = (blockIdx.x % p.head_blocks) * p.heads, heads = min(p.heads, a.n_heads - h0);
-  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), a.n_rows - row0));
-  const int n = p.heads * p.units, pair_units = r.span / 2 / E;
-  // threads side by side on a row's pieces, `side` rows at a time
-  const int side = n < kRopeOpThreads ? p.by_n(kRopeOpThreads) : 1;
-  const int t0 = n < kRopeOpThreads ? p.by_n(threadIdx.x) : 0;
-  int i = threadIdx.x - t0 * n, t = t0, d = 0, j = 0;
-  const T* src = nullptr;
-  T* dst = nullptr;
-  bool turns = false, pair = false;
-  auto piece = [&]() -> bool {             // what depends on the piece; false: none left
-    for (; i < n && t0 < side; i += kRopeOpThreads) {
-      const int h = p.by_units(i), u = i - h * p.units;
-      if (h >= heads) continue;
-      // half: pairs of pieces first, then the pieces that pass through
-      pair = HALF && u < pair_units;
-      d = HALF && !pair ? r.span + (u - pair_units) * E : u * E;
-      j = HALF ? d : d / 2;
-      turns = (!HALF || pair) && j < r.n_rot;
-      src = static_cast<const T*>(a.x) + (row0 + t0) * a.x_row + (h0 + h) * a.x_head + d;
-      dst = static_cast<T*>(a.out) + (row0 + t0) * a.out_row + (h0 + h) * a.out_head + d;
-      t = t0;
-      return t < rows;
+  // (rows of the CTA, groups of heads, pieces): side by side on the threads
+  const int block = blockIdx.x / p.chunks, n = p.groups * p.units;
+  int i = (blockIdx.x - block * p.chunks) * kDirectThreads + threadIdx.x, t0 = 0;
+  if (p.chunks == 1) t0 = p.by_n(i), i -= t0 * n;
+  if (i >= n || t0 >= p.side) return;
+  const int grp = p.by_units(i), u = i - grp * p.units, h0 = grp * p.heads, heads = min(p.heads, a.n_heads - h0);
+  // half: pairs of pieces first, then the pieces that pass through
+  const int pair_units = r.span / 2 / E;
+  const bool pair = HALF && u < pair_units;
+  const int d = HALF && !pair ? r.span + (u - pair_units) * E : u * E, j = HALF ? d : d / 2;
+  const int turning = !HALF || pair ? min(PP, r.n_rot - j) : 0;   // pairs of the piece that turn
+  uint64_t step[PP];
+#pragma unroll
+  for (int e = 0; e < PP; ++e) step[e] = e < turning ? r.step[j + e] : 0;
+  const int64_t first = static_cast<int64_t>(block) * p.side * p.rows + t0, last = min(first + p.side * p.rows, static_cast<int64_t>(a.n_rows));
+  const T* src0 = static_cast<const T*>(a.x) + h0 * a.x_head + d;
+  T* dst0 = static_cast<T*>(a.out) + h0 * a.out_head + d;
+  int pos = first < last ? a.positions[first] : -1;
+  for (int64_t row = first; row < last; row += p.side) {
+    const int at = pos;
+    if (row + p.side < last) pos = a.positions[row + p.side];
+    if (at < 0) continue;
+    const T* src = src0 + row * a.x_row;
+    T* dst = dst0 + row * a.out_row;
+    Piece<T> x0[B], x1[HALF ? B : 1];
+    auto load = [&](int h) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (h + b >= heads) break;
+        x0[b].v = __ldcs(reinterpret_cast<const uint4*>(src + (h + b) * a.x_head));
+        if (HALF && pair) x1[b].v = __ldcs(reinterpret_cast<const uint4*>(src + (h + b) * a.x_head + r.span / 2));
+      }
+    };
+    load(0);
+    float2 cs[PP];
+#pragma unroll
+    for (int e = 0; e < PP; ++e) {
+      float c = 1.f, s = 0.f;
+      if (turning > 0) rope_turn(at, step[e], static_cast<float>(r.magnitude), c, s);
+      cs[e] = make_float2(c, a.inverse ? -s : s);
     }
-    return false;
-  };
-  Piece<T> x0[B], x1[HALF ? B : 1];
-  auto load = [&]() {
+    for (int h = 0; h < heads; h += B) {
+      if (h > 0) load(h);
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (t + b * side >= rows) break;
-      x0[b].v = __ldcs(reinterpret_cast<const uint4*>(src + b * side * a.x_row));
-      if (HALF && pair) x1[b].v = __ldcs(reinterpret_cast<const uint4*>(src + b * side * a.x_row + r.span / 2));
-    }
-  };
-  bool some = piece();
-  if (some) load();
-  angles<PP>(r, a, p, row0, cs, pos);
-  while (some) {
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int tb = t + b * side;
-      if (tb >= rows) break;
-      if (turns) {
-        const float2* c = cs + tb * p.n_tab + j / PP;
-        const int ce = p.n_tab / PP;       // from a piece's pair to its next
-        if (j + PP <= r.n_rot) {
-#pragma unroll
-          for (int e = 0; e < PP; ++e) {
-            if (HALF) turn(x0[b].e[e], x1[b].e[e], c[e * ce]);
-            else turn(x0[b].e[2 * e], x0[b].e[2 * e + 1], c[e * ce]);
-          }
+      for (int b = 0; b < B; ++b) {
+        if (h + b >= heads) break;
+        if (turning == PP) {
+          turn_piece<T, HALF>(x0[b], x1[HALF ? b : 0], cs);
         } else {
 #pragma unroll
-          for (int e = 0; e < PP; ++e) {
-            if (j + e >= r.n_rot) break;
-            if (HALF) turn(x0[b].e[e], x1[b].e[e], c[e * ce]);
-            else turn(x0[b].e[2 * e], x0[b].e[2 * e + 1], c[e * ce]);
-          }
+          for (int e = 0; e < PP; ++e)
+            if (e < turning) turn(x0[b].e[HALF ? e : 2 * e], HALF ? x1[HALF ? b : 0].e[e] : x0[b].e[2 * e + 1], cs[e]);
         }
+        *reinterpret_cast<uint4*>(dst + (h + b) * a.out_head) = x0[b].v;
+        if (HALF && pair) *reinterpret_cast<uint4*>(dst + (h + b) * a.out_head + r.span / 2) = x1[b].v;
       }
-      if (pos[tb] < 0) continue;
-      *reinterpret_cast<uint4*>(dst + b * side * a.out_row) = x0[b].v;
-      if (HALF && pair) *reinterpret_cast<uint4*>(dst + b * side * a.out_row + r.span / 2) = x1[b].v;
     }
-    t += B * side;
-    src += B * side * a.x_row;
-    dst += B * side * a.out_row;
-    if (t >= rows) {
-      i += kRopeOpThreads;
-      some = piece();
-    }
-    if (some) load();
   }
 }
 
@@ -206,7 +233,7 @@ __global__ void __launch_bounds__(kRopeOpThreads) rope_staged_kernel(const __gri
     if (PIECES) reinterpret_cast<uint4*>(tile)[i] = *reinterpret_cast<const uint4*>(src);
     else tile[i] = *src;
   });
-  angles<1>(r, a, p, row0, cs, pos);
+  angles(r, a, p, row0, cs, pos);
   const bool half = r.layout == SPEC_ROPE_HALF;
   for (int i = threadIdx.x; i < p.rows * p.heads * r.n_rot; i += kRopeOpThreads) {
     const int rh = p.by_pairs(i), j = i - rh * r.n_rot, t = p.by_heads(rh);
@@ -231,37 +258,48 @@ cudaError_t launch_typed(const RopeArgs& r, const RopeOpArgs& a, cudaStream_t st
                       whole(a.x_head, a.n_heads) && whole(a.out_row, a.n_rows) && whole(a.out_head, a.n_heads);
   const bool half = r.layout == SPEC_ROPE_HALF;
   const bool direct = pieces && (!half || (r.span / 2) % E == 0);
-  // bytes of a CTA: enough in flight for many rows, spread over the SMs for few
-  const int64_t head = static_cast<int64_t>(a.dim) * sizeof(T), total = head * a.n_heads * a.n_rows;
-  int64_t bytes = total / (2 * 148);
-  const int64_t most = direct ? 2 * kRopeTile : kRopeTile;
-  bytes = bytes < 4096 ? 4096 : bytes > most ? most : bytes;
   RopePlan p{};
-  p.heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.n_heads, bytes / head)));
-  p.rows = p.heads < a.n_heads ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeRows, bytes / (head * a.n_heads))));
-  p.head_blocks = (a.n_heads + p.heads - 1) / p.heads;
   p.units = !direct ? (pieces ? a.dim / E : a.dim) : half ? r.span / 2 / E + (a.dim - r.span) / E : a.dim / E;
   if (direct && a.x == a.out)               // in place: only what turns
     p.units = half ? (r.n_rot + E - 1) / E : (2 * r.n_rot + E - 1) / E;
   if (p.units < 1) return cudaSuccess;
   p.by_units = make_div(p.units);
+  if (direct) {
+    // few rows: the heads spread over threads, down to one; many: all heads to a
+    // thread and up to 16 rows, so that angles and frequencies are formed and read
+    // once (half as wide 47.1 us for the case above, twice as wide 48.9)
+    const int64_t wide = 148 * 512, pieces_all = static_cast<int64_t>(a.n_rows) * a.n_heads * p.units;
+    p.heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.n_heads, pieces_all / wide)));
+    p.groups = (a.n_heads + p.heads - 1) / p.heads;
+    const int n = p.groups * p.units;
+    p.side = std::max(1, kDirectThreads / n);
+    p.chunks = (n + kDirectThreads - 1) / kDirectThreads;
+    p.rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, static_cast<int64_t>(a.n_rows) * n / (4 * wide))));
+    p.by_n = make_div(n);
+    const int64_t per = static_cast<int64_t>(p.side) * p.rows, ctas = (a.n_rows + per - 1) / per * p.chunks;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(ctas));
+    return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF>, grid, dim3(kDirectThreads), 0, st, r, a, p)
+                : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED>, grid, dim3(kDirectThreads), 0, st, r, a, p);
+  }
+  // bytes of a CTA: enough in flight for many rows, spread over the SMs for few
+  const int64_t head = static_cast<int64_t>(a.dim) * sizeof(T), total = head * a.n_heads * a.n_rows;
+  int64_t bytes = total / (2 * 148);
+  bytes = bytes < 4096 ? 4096 : bytes > kRopeTile ? kRopeTile : bytes;
+  p.heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.n_heads, bytes / head)));
+  p.rows = p.heads < a.n_heads ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeRows, bytes / (head * a.n_heads))));
+  p.head_blocks = (a.n_heads + p.heads - 1) / p.heads;
   p.by_heads = make_div(p.heads);
-  p.by_n = make_div(p.heads * p.units);
   p.by_pairs = make_div(std::max(r.n_rot, 1));
   const int64_t ctas = (static_cast<int64_t>(a.n_rows) + p.rows - 1) / p.rows * p.head_blocks;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(ctas)), block(kRopeOpThreads);
-  const int pp = !direct ? 1 : half ? E : E / 2;
-  p.n_tab = (r.n_rot + pp - 1) / pp * pp;
-  const size_t smem = static_cast<size_t>(p.rows) * p.n_tab * sizeof(float2);   // at most 32 KB
-  if (direct)
-    return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF>, grid, block, smem, st, r, a, p)
-                : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED>, grid, block, smem, st, r, a, p);
+  const dim3 grid(static_cast<unsigned>(ctas));
+  const size_t smem = static_cast<size_t>(p.rows) * r.n_rot * sizeof(float2);   // at most 32 KB
   // the staged form's tile comes on top
   auto kern = pieces ? rope_staged_kernel<T, true> : rope_staged_kernel<T, false>;
   static std::atomic<uint64_t> allowed[2] = {};
   const cudaError_t e = allow_smem(kern, kRopeRows * kMaxPairs * static_cast<int>(sizeof(float2)), allowed[pieces]);
-  return e != cudaSuccess ? e : launch_k(kern, grid, block, smem, st, r, a, p);
+  return e != cudaSuccess ? e : launch_k(kern, grid, dim3(kRopeOpThreads), smem, st, r, a, p);
 }
 
 }  // namespace
