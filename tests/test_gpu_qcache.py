@@ -264,16 +264,45 @@ def test_write_flags_what_it_cannot_store():
     c.same()
 
 
+@pytest.mark.parametrize("ties", [1.0, 0.02])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_write_of_keys_next_to_rounding_borders(ties, layout):
+    """Angles of 10^-9: keys that lie half way between two codes turn just off the border, and
+    the side decides.  All of them, and a few."""
+    H, D, n, block = 2, 256, 70, 64
+    c = Cache(5, [64, 3], n, H, D, block)
+    c.fill()
+    shape = (2, n, H, D)
+    border = (1 + (2 * c.rng.integers(0, 8, shape) + 1) / 16) * 2.0 ** c.rng.integers(-2, 3, shape)
+    x = np.where(c.rng.random(shape) < ties, border * c.rng.choice([-1.0, 1.0], shape), c.rng.normal(size=shape))
+    k, v = torch.from_numpy(x).to(torch.bfloat16).cuda(), c.rows(n, H)
+    kw = dict(scaling="linear", factor=1e12)
+    freq = Q.rope_frequencies(256, 128, 10000.0, **kw)
+    for b, L in enumerate(c.lens):
+        Q.append(c.k, c.ks, block, c.table[b], L, turned(k[b], L, freq, layout, 256))
+        Q.append(c.v, c.vs, block, c.table[b], L, v[b].double().cpu().numpy())
+    ws = workspace(B.spec_qcache_write_workspace_bytes(c.desc, 2, n))
+    B.spec_qcache_write(c.desc, rope_config(256, 128, layout, **kw), c.d["table"], c.max_pages, c.d["lens"], 2, n, k,
+                        H * D, v, H * D, ws, ws.numel())
+    c.same()
+
+
 # ----------------------------------------------------------------- attention
 
 def attention_bound(out, spread, mass, tail):
     """Half a bf16 step of the result; the queries' two codes keep each to 2^-8 of
     itself, which moves score j by at most 2^-8 e_j and so its weight by that
     share (spread); each weight's two codes are off by 2^-8 of it (mass) and, the
-    smallest, by 2^-21 of the largest weight, each key's values up to the block's
-    largest (tail); sums and exponentials in binary32 cost 2^-16 of the mass."""
+    smallest, by 2^-19 of the largest weight, each key's values up to the block's
+    largest (tail); sums and exponentials in binary32 cost 2^-16 of the mass.
+
+    2^-19: a weight w (1 for the row's reference, which the largest weight is not
+    below) is coded as 32 w = w0 + w1 / 16.  The least step of e4m3 is 2^-9, so w1
+    is off by up to 2^-10, 32 w by 2^-14 and w by 2^-19.  2^-8: 32 w in binary16 is
+    off by 2^-11 of itself, w0 leaves at most 2^-4 of the power of two below 32 w,
+    and w1 half a step of the 2^-5 below that, 2^-9: 2^-9 + 2^-11 < 2^-8."""
     return (HALF_BF16 * np.abs(out) + 1.1 * 2.0 ** -8 * spread + (2.0 ** -8 + 2.0 ** -16) * mass
-            + 2.0 ** -21 * tail + 1e-30)
+            + 2.0 ** -19 * tail + 1e-30)
 
 
 def check_attention(c, q, got, cfg_args, q_offset, extra, window, scale=None, table=None):
@@ -451,6 +480,98 @@ def test_rows_do_not_depend_on_the_rows_beside_them():
             B.spec_qcache_attn(c.desc, cfg, row[1:], 2048, 8, table[1:], c.max_pages, at[1:], 1, 1, 0, 1, window, 0.0,
                                one, ws, ws.numel())
             assert torch.equal(one[0, 0], out[1, i]), (window, i)
+
+
+def attend(c, cfg, q, Hq, n, window=0, stream=None, extra=None, table=None, ws=None, lens=None):
+    """spec_qcache_attn of n cached tokens on a workspace of its own; the result."""
+    table, lens = c.d["table"] if table is None else table, c.d["lens"] if lens is None else lens
+    batch, max_pages = table.shape
+    if ws is None:
+        ws = workspace(B.spec_qcache_attn_workspace_bytes(c.desc, Hq, batch, n, max_pages, window))
+    out = torch.empty_like(q)
+    B.spec_qcache_attn(c.desc, cfg, q, Hq * c.D, Hq, table, max_pages, lens, batch, n, 0, n if extra is None else extra,
+                       window, 0.0, out, ws, ws.numel(), stream)
+    return out
+
+
+@pytest.mark.parametrize("window", [0, 60])
+def test_attention_of_many_ragged_sequences(window):
+    """More sequences than a warp has lanes, most of them short, some empty."""
+    lens = [int(x) for x in np.random.default_rng(17).integers(0, 150, 75)]
+    lens[3], lens[40], lens[70], lens[74] = 0, 700, 0, 128
+    c = Cache(17, lens, 1, 2, 128, 32, 128)
+    c.fill()
+    q = c.rows(2, 6)
+    out = attend(c, None, q, 6, 2, window, extra=0)
+    check_attention(c, q, out, (Q.rope_frequencies(2, 0), "half", 2, 1.0), 0, 0, window)
+
+
+def test_results_depend_neither_on_the_table_s_width_nor_on_who_shares_a_page():
+    """One split and its join: the same bits from a wider table; a prefix shared by two sequences."""
+    c = Cache(18, [100, 100], 4, 2, 256, 16, 128)
+    c.fill()
+    c.d["lens"] -= 4                                    # the rows are the cache's last four
+    cfg, q = rope_config(256, 128), c.rows(4, 8)
+    narrow = attend(c, cfg, q, 8, 4)
+    wide = torch.full((2, 64), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.max_pages] = c.d["table"]
+    assert torch.equal(attend(c, cfg, q, 8, 4, table=wide), narrow)
+    shared = c.d["table"].clone()
+    shared[1] = shared[0]
+    q[1] = q[0]
+    both = attend(c, cfg, q, 8, 4, table=shared)
+    assert torch.equal(both[0], narrow[0]) and torch.equal(both[1], narrow[0])
+
+
+def test_pools_past_four_gigabytes():
+    """Pages whose offsets in bytes pass 32 bits: append and attention."""
+    lens, n, Hq, H, D, block = [200, 61], 5, 16, 8, 256, 32
+    c = Cache(19, lens, n, H, D, block, 128)
+    c.fill()
+    P = c.k.shape[0]
+    N = 2 ** 32 // (H * 64 * D) + 500
+    big = {m: torch.zeros((N, H, 64, D), dtype=torch.uint8, device="cuda") for m in ("k", "v")}
+    big.update({m: torch.zeros((N, H, 64 // block), dtype=torch.float32, device="cuda") for m in ("ks", "vs")})
+    for m, t in big.items():
+        t[N - P:] = c.d[m]
+        c.d[m] = t[N - P:]
+    c.d["table"] += N - P
+    c.desc = B.SpecQCache(D, H, N, 64, block, 128, *(big[m].data_ptr() for m in ("k", "v", "ks", "vs")))
+    k, v, q = c.rows(n, H), c.rows(n, H), c.rows(n, Hq)
+    freq, cfg = Q.rope_frequencies(256, 64), rope_config(256, 64)
+    ws = workspace(B.spec_qcache_attn_workspace_bytes(c.desc, Hq, 2, n, c.max_pages, 0))
+    out = torch.empty_like(q)
+    B.spec_qcache_verify_attn(c.desc, cfg, q, Hq * D, Hq, k, H * D, v, H * D, c.d["table"], c.max_pages, c.d["lens"], 2,
+                              n, 0, 0.0, out, ws, ws.numel())
+    assert B.spec_read_device_status(ws, ws.numel()) == 0
+    for b, L in enumerate(lens):
+        Q.append(c.k, c.ks, block, c.table[b], L, turned(k[b], L, freq, "half", 256))
+        Q.append(c.v, c.vs, block, c.table[b], L, v[b].double().cpu().numpy())
+    c.same()
+    check_attention(c, q, out, (freq, "half", 256, 1.0), 0, n, 0)
+    assert not big["k"][:N - P].any() and not big["v"][:N - P].any()
+
+
+def test_two_calls_at_once_and_a_workspace_used_again():
+    """Calls on two streams with workspaces of their own; then different shapes in turn on one."""
+    c = Cache(20, [700, 300, 40], 20, 2, 128, 16, 128)
+    c.fill()
+    c.d["lens"] -= 20
+    cfg = rope_config(128, 64)
+    qs = [c.rows(n, 8) for n in (1, 5, 17, 20)]
+    want = [attend(c, cfg, q, 8, q.shape[1]) for q in qs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [workspace(B.spec_qcache_attn_workspace_bytes(c.desc, 8, 3, 20, c.max_pages, 0)) for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(attend(c, cfg, qs[i % 4], 8, qs[i % 4].shape[1], stream=streams[i % 2], ws=spaces[i % 2]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 4]) for i, g in enumerate(got))
+    for i in (3, 0, 2, 1, 3):
+        assert torch.equal(attend(c, cfg, qs[i], 8, qs[i].shape[1], ws=spaces[0]), want[i])
+    assert all(B.spec_read_device_status(ws, ws.numel()) == 0 for ws in spaces)
 
 
 # ------------------------------------------------------------------ together
