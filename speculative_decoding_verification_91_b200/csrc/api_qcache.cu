@@ -77,7 +77,7 @@ int rope_args(const spec_rope_config* r, int head_dim, RopeArgs* a) {
   a->magnitude = r->magnitude;
   for (int j = 0; j < r->n_rot; ++j) {
     const double turns = f[j] / (2.0 * M_PI);
-    a->step[j] = static_cast<uint64_t>(ldexp(turns - floor(turns), 64));   // below 2^64: the fraction is below 1
+    a->step[j] = static_cast<uint64_t>((turns - floor(turns)) * 0x1p64);   // below 2^64: the fraction is below 1
   }
   return SPEC_OK;
 }

@@ -616,6 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       __syncwarp();
       return true;
     };
+    // rows of P that no query row owns stay zero (what they held cost power: P V is
+    // done for all 128)
+    for (int i = st; i < PB * static_cast<int>(kPBytes) / 16; i += kSoftWarps * 32)
+      reinterpret_cast<uint4*>(pbuf)[i] = make_uint4(0, 0, 0, 0);
+    named_bar(1, kSoftWarps * 32);
     pdl_wait();
     bool have_item = take(0);
     int item = 0;
