@@ -37,7 +37,8 @@
 // are zeroed in shared memory before P V, so stale slots (NaN codes among them)
 // never reach it.  Key blocks start at absolute multiples of 128 and a row's
 // weights depend on its own scores only, so a row's partial depends neither on n
-// nor on the batch, its row slot or the CTA.  Every wait is bounded.
+// nor on the batch, its row slot or the CTA: sums of p are kept by 16 keys of a
+// block, whatever RP, and added in key order.  Every wait is bounded.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -60,7 +61,7 @@ constexpr int kFirstSoft = 4;
 constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
 constexpr uint32_t kSmemMax = 227u * 1024u;
 constexpr int kItems = 4;                  // items described ahead in shared memory
-constexpr uint32_t kTail = 16384;
+constexpr uint32_t kTail = 16896;
 constexpr uint32_t kPBytes = 128 * kBlk;
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
 constexpr int kMaxPg = 256;                // its pages: 16384 keys / 64
@@ -250,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   Item* items = reinterpret_cast<Item*>(tail + 512);       // [kItems]
   float* red = reinterpret_cast<float*>(tail + 1024);      // [threads of a row][rows]
   float* alpha_s = red + 256;                              // [rows]
-  float* l_s = alpha_s + 64;                               // [threads of a row][rows]: sums of p
-  float* bad_s = l_s + 256;                                // [rows]
-  float* ks_s = reinterpret_cast<float*>(tail + 4096);     // [kItems][kMaxScales]
+  float* l_s = alpha_s + 64;                               // [16 keys of a block][rows]: sums of p
+  float* bad_s = l_s + 512;                                // [rows]
+  float* ks_s = reinterpret_cast<float*>(tail + 4608);     // [kItems][kMaxScales]
   float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
   int* pg_s = reinterpret_cast<int*>(vs_s + kItems * kMaxScales);   // [kItems][kMaxPg]; < 0: not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -624,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     pdl_wait();
     bool have_item = take(0);
     int item = 0;
-    float l_was = 0.f, m_was = 0.f;                   // of the item before
+    constexpr int NE = KW / 16;                       // 16-key groups of a thread (one scale each, and one sum)
+    float l_was[NE] = {}, m_was = 0.f;                // of the item before
     bool bad_was = false;
     // Ends the item before: (m, l) and o = (o0 + o1 / 16) / kUnit.  Loads of 16
     // lanes leave w0's and w1's sums of a row and a column in one thread (rows lane
@@ -632,14 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     auto finish = [&]() {
       const Item& x = items[(item - 1) % kItems];
       wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-      l_r[grp * RP + lane] = l_was;
+#pragma unroll
+      for (int u = 0; u < NE; ++u) l_r[(grp * NE + u) * RP + lane] = l_was[u];
       if (grp == 0) bad_s[row] = bad_was ? 1.f : 0.f;
       named_bar(1, kSoft);
       tc_fence_after();
       if (grp == 0 && row < x.nrows && a.n_splits > 1 && !*fail) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < NG; ++e) sum += l_r[e * RP + lane];
+        for (int e = 0; e < NG * NE; ++e) sum += l_r[e * RP + lane];
         __stcg(&a.part_ml[x.slot + row], make_float2(m_was, sum));
       }
       if (quad * RQ < x.nrows) {
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             dst[i] = a.out + ((x.out0 + pos) * (a.c.n_kv_heads * a.G) + x.h * a.G + (x.r0 + r - pos * a.G)) * D + lane % 4 * 2;
             sum[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < NG; ++e) sum[i] += l_s[e * RP + r];
+            for (int e = 0; e < NG * NE; ++e) sum[i] += l_s[e * RP + r];
             if (bad_s[r] != 0.f) sum[i] = __int_as_float(0x7fffffff);    // a NaN query
           }
         }
@@ -724,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const float* ks = ks_s + (item % kItems) * kMaxScales;
       const float* vs = vs_s + (item % kItems) * kMaxScales;
       if (more) wait(&sc_full[item % kItems], (item / kItems) & 1);
-      float mref = kNoKey, l = 0.f;
+      float mref = kNoKey, l[NE] = {};
       for (int j = 0; j < nb; ++j, ++g) {
         const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;
-        constexpr int NE = KW / 16;                   // scales of the keys (one or two of 16-token blocks)
         float s[KW], f[NE], vsc[NE], cand = -INFINITY;
         uint32_t w0[KW / 4], w1[KW / 4];
         if (more) {
@@ -782,7 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             if (mine && bm > mref + kLazy) {
               al = ex2(mref - bm);              // 0 while the row had no key
               mref = bm;
-              l *= al;
+#pragma unroll
+              for (int u = 0; u < NE; ++u) l[u] *= al;
             }
             if (j > 0) {
               // the running sums of the rows that moved (all earlier P V done)
@@ -814,8 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             for (int c = 0; c < KW; c += 2) {
               const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
               const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
-              l += p0;
-              l += p1;
+              l[c >> 4] += p0;
+              l[c >> 4] += p1;
               const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
               uint16_t c0, c1;
               uint32_t back;
@@ -867,7 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
       if (!more) break;
-      l_was = l;
+#pragma unroll
+      for (int u = 0; u < NE; ++u) l_was[u] = l[u];
       m_was = mref;
       bad_was = bad_q;
       have_item = take(item + 1);

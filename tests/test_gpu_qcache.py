@@ -574,6 +574,23 @@ def test_two_calls_at_once_and_a_workspace_used_again():
     assert all(B.spec_read_device_status(ws, ws.numel()) == 0 for ws in spaces)
 
 
+def test_few_and_many_rows_give_the_same_bits():
+    """Steps of one and of five rows take row blocks of different heights: 500,000 results, to the bit."""
+    B_, Hq, H, D = 16, 32, 4, 256
+    c = Cache(21, list(range(1200, 1200 + B_)), 5, H, D, 64, 512)
+    c.fill()
+    q = c.rows(5, Hq)
+    five = attend(c, None, q, Hq, 5, extra=0)
+    for i in range(5):
+        # (q_offset i and no new key: the row sees what it saw among the five)
+        out = torch.empty(B_, 1, Hq, D, dtype=torch.bfloat16, device="cuda")
+        row = q[:, i].contiguous()
+        ws = workspace(B.spec_qcache_attn_workspace_bytes(c.desc, Hq, B_, 1, c.max_pages, 0))
+        B.spec_qcache_attn(c.desc, None, row, Hq * D, Hq, c.d["table"], c.max_pages, c.d["lens"], B_, 1, i, 0, 0, 0.0,
+                           out, ws, ws.numel())
+        assert torch.equal(out[:, 0], five[:, i]), i
+
+
 # ------------------------------------------------------------------ together
 
 def test_a_decode_loop_on_another_stream_and_in_a_graph():
