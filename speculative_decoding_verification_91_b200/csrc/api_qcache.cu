@@ -108,9 +108,10 @@ struct AttnLayout {
 // Split of a call's attention.  Verify and decode calls (n <= SPEC_MAX_K + 1) take
 // the cache's, so that a row's result depends on neither n nor the batch.  A
 // prompt chunk has row blocks enough to fill the GPU, and a split's partial
-// results cost it more than they give (256 rows over 8k of context, 32 / 4
-// heads: 84 MB of them): it takes the longest split that still leaves four
-// items an SM, up to the kernel's limit of 256 scales.
+// results and its join cost it more than they give (256 rows over 8k of context,
+// 32 / 4 heads: 296 us in three splits, 230 in one, which needs no join): it takes
+// the number of splits of the least cost below, up to four items an SM and the
+// kernel's limit of 256 scales an item.
 constexpr int kItemsWanted = 4 * 148;
 int call_split(const spec_qcache* c, int n_q_heads, int64_t B, int n, int max_pages) {
   const int split = split_of(c);

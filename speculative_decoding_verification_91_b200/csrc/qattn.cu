@@ -20,7 +20,7 @@
 //              from TMEM, B = K, K-major).  With Q in shared memory too the two
 //              operands took all of its bandwidth.
 //   warp 2     finds the CTA's items and describes them in shared memory, with
-//              their scales, up to kItems ahead.
+//              their pages and then their scales, up to kItems ahead.
 //   warp 3     one thread issues O[rows][dim] += P V (A = P in shared memory,
 //              K-major, B = V as stored, MN-major).
 //   warps 4-11 softmax: a thread takes one query row and RP / 2 of the block's
@@ -32,6 +32,17 @@
 //              barrier vote per block); the v scale is folded into m and p
 //              (p v_scale <= 2^kLazy), so blocks of any scale share one
 //              accumulator; the sum of p is kept in binary32.
+//
+// Per block of 128 keys (D = 256), in SM clocks: the scores' MMAs 1024, P V 512, a
+// softmax warp 1650 with RP = 32 and 2350 with RP = 64 (exponentials and codes 930,
+// the largest score 250, the store of P 270, the rest latency between them), DRAM
+// 2840 with every SM at work.  So long items of few rows run at the pace of DRAM
+// (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 425 us, 5.4 TB/s, the clock down
+// to 1.45 GHz at the power limit), prompt chunks at that of the softmax (256 rows
+// over 8k, 32 / 4 heads, 2 sequences: 230 us, tensor pipe 54% busy), and calls of
+// some items a CTA also pay for the unequal shares of whole splits.  Not kept: 16
+// softmax warps, a vote after the exponentials instead of before (3% slower), a
+// larger kLazy (1 to 4% faster, coarser small weights).
 //
 // Value rows of keys outside the item's range or on pages that were not loaded
 // are zeroed in shared memory before P V, so stale slots (NaN codes among them)
@@ -1076,6 +1087,9 @@ cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
   e = D == 256 ? launch_dim<256>(rp, grid, tk, tv, a, st) : launch_dim<128>(rp, grid, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   if (a.n_splits == 1) return cudaSuccess;     // the results are out
+  // few splits: one thread has them all in flight; more: four threads; very many of
+  // few rows: one dim a thread, for more CTAs (131k tokens, 36 rows of 129 splits: 10.5
+  // us against 20 for four dims; 8 sequences of 33: 16 against 64)
   if (a.n_splits <= 4) return launch_combine<1, 4, 4>(a, st);
   if (a.n_splits <= 8) return launch_combine<1, 4, 8>(a, st);
   const int64_t all = static_cast<int64_t>(a.B) * a.c.n_kv_heads * a.rows;

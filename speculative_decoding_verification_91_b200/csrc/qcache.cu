@@ -54,7 +54,10 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // hold the block's new rows in registers (a lane 8 dims, IT rows of each warp), find
 // the largest magnitude, settle the scale and store the codes, the next head's rows
 // on their way meanwhile; every row is read once.  The angles of the block's rows are
-// formed once, in shared memory.  Bound by instruction issue and latency: TUNED
+// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 75 us, 2.7 TB/s,
+// bound by instruction issue (59% of the slots with 16 warps an SM, which the rows in
+// registers allow): the second set of codes costs 10 us of it, the angles 8.  512
+// threads a CTA, or three CTAs an SM, spill (103 and 119 us).
 //
 // Codes are those of the exactly turned key.  Keys turn in binary32, off by less
 // than kTurnErr (|x0| + |x1|) magnitude: cosine and sine 1.5 steps and a rounding by
@@ -321,7 +324,8 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
 // row with an infinity or NaN gets a NaN scale, which makes its result NaN.
 // A CTA takes a row of a sequence and every blockIdx.y-th four of its heads, a warp a head (4 or
 // 8 dims a lane): the row's angles once for all of them (each warp forming its own took 41 us
-// instead of TUNED for 512 rows of 32 heads), the first head asked for before.
+// instead of 16 for 512 rows of 32 heads), the first head asked for before.  Few rows: 4.5 us,
+// most of it under the split kernel's start.
 template <int D>
 __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant__ RopeArgs r,
                                                            const __grid_constant__ QAttnArgs a) {
