@@ -400,7 +400,8 @@ int spec_rope_frequencies(const spec_rope_config* r, int head_dim, double* out);
  * negative is a padding row: its out is left as it was.  inverse != 0 turns
  * back (the transpose: also the gradient of x given that of out).  out may be x
  * with the same strides; otherwise the two must not overlap.  Angles are formed
- * in binary64, products and sums in binary32, results rounded once.
+ * as fractions of a turn in steps of 2^-64, cosines, products and sums in
+ * binary32, results rounded once.
  * head_dim 2..SPEC_ROPE_MAX_DIM; pointers aligned to their element type. */
 int spec_rope(const spec_rope_config* r, int dtype, const void* x, int64_t x_row_stride,
               int64_t x_head_stride, void* out, int64_t out_row_stride, int64_t out_head_stride,

@@ -314,9 +314,9 @@ int spec_rope(const spec_rope_config* r, int dtype, const void* x, int64_t x_row
   if (x_row_stride < 0 || x_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0) return SPEC_EINVAL;
   // the written heads and rows must be apart, in either order of nesting
   const bool by_row = (n_heads == 1 || out_head_stride >= head_dim) &&
-                      (n_rows == 1 || out_row_stride >= (n_heads - 1) * out_head_stride + head_dim);
+                      (n_rows == 1 || out_row_stride >= (__int128)(n_heads - 1) * out_head_stride + head_dim);
   const bool by_head = (n_rows == 1 || out_row_stride >= head_dim) &&
-                       (n_heads == 1 || out_head_stride >= (n_rows - 1) * out_row_stride + head_dim);
+                       (n_heads == 1 || out_head_stride >= (__int128)(n_rows - 1) * out_row_stride + head_dim);
   if (!by_row && !by_head) return SPEC_EINVAL;
   if (x == out && ((n_rows > 1 && x_row_stride != out_row_stride) ||
                    (n_heads > 1 && x_head_stride != out_head_stride)))
