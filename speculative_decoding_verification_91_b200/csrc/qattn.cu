@@ -99,6 +99,10 @@ __device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&v)[16])
                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&v)[32]) {
+  tmem_ld16x256(taddr, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+  tmem_ld16x256(taddr + 32, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -676,33 +680,32 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             if (bad_s[r] != 0.f) sum[i] = __int_as_float(0x7fffffff);    // a NaN query
           }
         }
-        // 32 columns at a time, the next ones asked for before these are stored
+        // 64 columns of eight rows at a time, or 32 of 16
         auto readout = [&](auto direct) {
-          const int c_first = cg * (D / 2), c_end = c_first + D / 2;
-          uint32_t o[NR][16];
-          auto load = [&](int c0) {
+          constexpr int NC = 64 / NR, NK = NC / 8;
+#pragma unroll 1
+          for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += NC) {
+            uint32_t o[NR][NC / 2];
 #pragma unroll
             for (int i = 0; i < NR; ++i) tmem_ld16x256(t_lane + (static_cast<uint32_t>(16 * i) << 16) + c0, o[i]);
-          };
-#pragma unroll 1
-          for (int c0 = c_first; c0 < c_end; c0 += 32) {
-            float2 y[NR][4];
-            load(c0);
 #pragma unroll
             for (int i = 0; i < NR; ++i) tmem_ld_wait_for(o[i]);
+            float2 y[NR][NK];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < NK; ++k)
 #pragma unroll
               for (int i = 0; i < NR; ++i) {
                 const int e0 = 4 * k + 2 * i, e1 = NR == 2 ? e0 : 4 * k + 2;
-                y[i][k].x = fmaf(__uint_as_float(o[NR - 1][e1]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0]) * (1.f / kUnit));
-                y[i][k].y = fmaf(__uint_as_float(o[NR - 1][e1 + 1]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0 + 1]) * (1.f / kUnit));
+                const auto sum_of = [&](int z) {
+                  return fmaf(__uint_as_float(o[NR - 1][e1 + z]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0 + z]) * (1.f / kUnit));
+                };
+                y[i][k] = make_float2(sum_of(0), sum_of(1));
               }
 #pragma unroll
             for (int i = 0; i < NR; ++i)
               if (have[i]) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < NK; ++k)
                   if constexpr (decltype(direct)::value)
                     *reinterpret_cast<uint32_t*>(dst[i] + c0 + 8 * k) =
                         sum[i] == 0.f ? 0u : pack_bf16x2(y[i][k].x / sum[i], y[i][k].y / sum[i]);
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             }
             __syncwarp();
           }
-          if (bar_red_or(1, kSoft, mine && cand > mref + kLazy)) {
+          if (j == 0 || bar_red_or(1, kSoft, mine && cand > mref + kLazy)) {
             red_r[grp * RP + lane] = cand;
             named_bar(1, kSoft);
             float bm = red_r[lane];
