@@ -151,10 +151,10 @@ bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_page
   const uint64_t rows = (uint64_t)B * n * n_q_heads;     // (sequence, KV head, row)
   if (rows > 0x3fffffffull) return false;
   // what the kernels count and divide in 32 bits: rows of a KV head by its query
-  // heads, and the key blocks of all (sequence, KV head, row block)
+  // heads, and twice the key blocks and items of all (sequence, KV head, row block)
   const uint64_t G = n_q_heads / c->n_kv_heads, per_head = n * G;
   if (per_head * G > 0xffffffffull ||
-      (uint64_t)B * c->n_kv_heads * ((per_head + 31) / 32) * ((uint64_t)max_pages / 2 + 1) > 0x7fffffffull)
+      (uint64_t)B * c->n_kv_heads * ((per_head + 31) / 32) * ((uint64_t)max_pages + 2) > 0x3fffffffull)
     return false;
   const uint64_t slots = rows * s->n_splits, D = c->head_dim;
   size_t off = kWsHeaderBytes;
@@ -274,6 +274,7 @@ int run_attn(const spec_qcache* c, const RopeArgs& r, const AttnCall& k, const A
   a.window = k.window;
   a.split = s.split;
   a.by_split = make_div(s.split / kQBlk);   // up to 2^7 of at most 2^23 blocks
+  a.by_cost = make_div(s.split / kQBlk + 1);
   a.by_G = make_div(a.G);
   a.n_splits = s.n_splits;
   a.q = static_cast<const uint16_t*>(k.q);

@@ -13,7 +13,7 @@
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
-// that start in an equal share of all key blocks.  12 warps:
+// whose middle lies in an equal share of their cost.  12 warps:
 //   warp 0     TMA producer: keys and values of 128-key blocks (two pages) into
 //              a ring of kUnits units of 128 x dim bytes.
 //   warp 1     allocates TMEM; one thread issues S[128][128 keys] = Q K^T (A = Q
@@ -168,7 +168,7 @@ struct Walker {
   int b, h, rb, sidx, L;
   int split0, p0, p1;      // the sequence's first split; positions of the row block's first and last row
   SeqKeys k;
-  int base, end, pos;      // key blocks before (b, h, rb); where the CTA stops; this item's start
+  int base, end, pos;      // cost before (b, h, rb); where the CTA stops; this item's middle
   int lo, hi, blk0, nb;    // this item's keys and blocks (nb = 0: none)
   bool fresh;
   __device__ bool valid() const { return b < a->B && pos < end; }
@@ -186,7 +186,8 @@ struct Walker {
       fresh = true;
     }
     const int s0 = (split0 + sidx) * a->split, start = max(s0, k.lo);
-    pos = base + ((start >> kLgBlk) - (k.lo >> kLgBlk));
+    const int b0 = start >> kLgBlk, b1 = min(s0 + a->split - 1, k.hi) >> kLgBlk;
+    pos = base + 2 * (b0 - (k.lo >> kLgBlk) + sidx) + (b1 - b0 + 2);
     lo = a->window > 0 ? max(start, p0 - a->window + 1) : start;
     hi = min(min(s0 + a->split - 1, k.hi), p1);
     blk0 = lo >> kLgBlk;
@@ -197,7 +198,7 @@ struct Walker {
     if (++sidx >= k.splits) {     // the next (b, h, rb) that has keys
       rows = true;
       sidx = 0;
-      base += k.blocks;
+      base += k.cost();
       if (++rb == RB) {
         rb = 0;
         if (++h == a->c.n_kv_heads) {
@@ -438,12 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   } else if (warp == 2) {
     // --------------------------------------------------- items and scales
     const int RB = (a.rows + RP - 1) / RP, per_b = a.c.n_kv_heads * RB;
-    // this CTA's share [x0, x1) of all key blocks and its first item
+    // this CTA's share [x0, x1) of the cost of all items and its first item
     const auto length = [&](int b) { return b < a.B ? __ldcg(&a.c.seq_lens[b]) : 0; };
-    const auto blocks = [&](int b, int L) { return b < a.B ? seq_keys(a, L).blocks * per_b : 0; };
-    int L = length(lane), n = blocks(lane, L), total = 0;
+    const auto cost = [&](int b, int L) { return b < a.B ? seq_keys(a, L).cost() * per_b : 0; };
+    int L = length(lane), n = cost(lane, L), total = 0;
     for (int b = lane; b - lane < a.B; b += 32) {
-      if (b >= 32) n = blocks(b, L = length(b));
+      if (b >= 32) n = cost(b, L = length(b));
       if (blockIdx.x == 0 && b < a.B &&
           (L < 0 || static_cast<int64_t>(L) + a.kv_extra > static_cast<int64_t>(a.c.max_pages) * kPg))
         flag_status(a.c.status, SPEC_DEV_BAD_LENGTH);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     w.end = x1;
     int pre = 0;
     for (int b = lane; b - lane < a.B && w.b == a.B && x1 > x0; b += 32) {
-      if (a.B > 32) n = blocks(b, L = length(b));
+      if (a.B > 32) n = cost(b, L = length(b));
       int incl = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -477,20 +478,18 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       pre += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (w.b < a.B) {
-      const int rem = x0 - w.base, hr = rem / w.k.blocks, r = rem - hr * w.k.blocks;
+      const int rem = x0 - w.base, hr = rem / w.k.cost(), r = rem - hr * w.k.cost();
       w.h = hr / RB;
       w.rb = hr - w.h * RB;
-      w.base += hr * w.k.blocks;
-      // the first split that starts at or after block r of the sequence
+      w.base += hr * w.k.cost();
+      // the first split whose middle is at or after cost r of the sequence: no middle
+      // of a split before the one that cost r falls into is
       const int first = w.k.lo >> kLgBlk, bps = a.split >> kLgBlk;
-      w.sidx = r == 0 ? 0 : static_cast<int>(a.by_split(r + first + bps - 1)) - w.split0;
-      if (w.sidx < w.k.splits) {
-        w.derive(true);
-      } else {
-        w.sidx = w.k.splits - 1;
-        w.fresh = true;
-        w.next();
-      }
+      w.sidx = static_cast<int>(a.by_cost(r / 2 + (first - w.split0 * bps)));
+      w.sidx = min(w.sidx, w.k.splits - 1);
+      w.derive(true);
+      while (w.b < a.B && w.pos < x0) w.next();
+      w.fresh = true;
     }
     const int lg_bt = 31 - __clz(a.c.block), lg_pg = 31 - __clz(kPg);
     bool fresh = true;

@@ -102,7 +102,7 @@ struct QAttnArgs {
   QCacheArgs c;
   int B, n, G, rows;            // rows = n * G per (sequence, KV head)
   int q_offset, kv_extra, window, split, n_splits;
-  Div by_split, by_G;           // of key blocks by those of a split; of rows by G
+  Div by_split, by_cost, by_G;  // of key blocks by those of a split, and by one more; of rows by G
   const uint16_t* q;
   int64_t q_row;
   float scale_log2;             // softmax scale * log2(e)
@@ -116,6 +116,8 @@ struct QAttnArgs {
 constexpr int kQBlk = 128;   // keys of one MMA block
 struct SeqKeys {
   int lo, hi, splits, blocks;
+  // in halves of a key block's time; an item's start and end take about a block's
+  __device__ int cost() const { return 2 * (blocks + splits); }
 };
 __device__ __forceinline__ SeqKeys seq_keys(const QAttnArgs& a, int L) {
   SeqKeys k{0, -1, 0, 0};
