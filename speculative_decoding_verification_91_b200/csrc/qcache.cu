@@ -109,10 +109,6 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
   const int p0 = (L / BT + static_cast<int>(blockIdx.x)) * BT;   // first position of the block
   if (p0 >= L + a.n) return;
   const int page = c.block_table[static_cast<int64_t>(b) * c.max_pages + p0 / kPg];
-  if (page < 0 || page >= c.num_pages) {
-    if (threadIdx.x == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
-    return;
-  }
   const int lo = max(p0, L) - p0, hi = min(BT, L + a.n - p0);    // new rows of the block
   const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, c.n_kv_heads);
   const int64_t stride = is_v ? a.v_row : a.k_row;
@@ -129,6 +125,10 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
       raw[i] = there >> i & 1 ? __ldg(reinterpret_cast<const uint4*>(p + i * RI * stride)) : make_uint4(0, 0, 0, 0);
   };
   load(h0);
+  if (page < 0 || page >= c.num_pages) {     // (looked up beside the first rows)
+    if (threadIdx.x == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
+    return;
+  }
   if (threadIdx.x == 0) list_n = 0;
   const bool half = r.layout == SPEC_ROPE_HALF, turns_keys = !is_v && r.n_rot > 0;
   const int hs = r.span / 2;
