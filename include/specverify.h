@@ -462,7 +462,8 @@ size_t spec_qcache_write_workspace_bytes(const spec_qcache* c, int max_batch, in
  * A sequence that does not fit its block-table row (or a negative length) sets
  * SPEC_DEV_BAD_LENGTH and is skipped; a page id outside the pool sets
  * SPEC_DEV_BAD_PAGE and that block is skipped.  No two sequences may write the
- * same page in one call.  n = 0 is valid and does nothing. */
+ * same page in one call, and no page may stand twice among those that one
+ * writes.  n = 0 is valid and does nothing. */
 int spec_qcache_write(const spec_qcache* c, const spec_rope_config* r, const int32_t* block_table,
                       int max_pages, const int32_t* seq_lens, int B, int n, const void* k_new,
                       int64_t k_row_stride, const void* v_new, int64_t v_row_stride, void* ws,
