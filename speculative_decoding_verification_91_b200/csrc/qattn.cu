@@ -309,14 +309,20 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   // before it is done (it triggers after its own wait), so what it does not write
   // itself is final, and nothing earlier still reads the partials.  (Those loads
   // pass by L1, which nothing has ordered yet.)
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // Barriers and TMEM are there once all warps have passed this; warp 2 comes with
+  // its first item in hand.
+  uint32_t tmem = 0;
+  const auto ready = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem = *tmem_slot;
+  };
   const auto wait = [&](uint64_t* bar, uint32_t parity) { return fwait(bar, parity, a.c.status, fail); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    ready();
     if (lane == 0) {
       // keys shared by several row blocks: normal priority in L2
       const uint64_t pol = a.rows > RP ? policy_evict_normal() : policy_evict_first();
@@ -375,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- scores
+    ready();
     if (lane == 0) {
       const uint32_t id_qk = idesc_e4m3(kBlk, false);
       int s = 0, su = 0, g = 0, nq = 0;     // ring slot and its round, block, query groups begun
@@ -406,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- P V
+    ready();
     // (a thread of its own: one thread that issued both spent 600 clocks from
     // the last MMA of one product to the first of the other)
     if (lane == 0) {
@@ -546,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         }
       }
       __syncwarp();
+      if (i == 0) ready();
       if (lane == 0) mbar_arrive(&it_full[q]);
       if (!end) {
         fresh = false;
@@ -569,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------- softmax
+    ready();
     constexpr int KW = RP / 2;                 // keys of a block a thread takes
     constexpr int NG = kBlk / KW;              // threads of a row
     const int quad = warp & 3, cg = (warp - kFirstSoft) >> 2;     // TMEM lane quadrant; first or second half of its keys
