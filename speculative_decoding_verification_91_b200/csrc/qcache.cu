@@ -82,25 +82,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return m;
 }
 
-template <int D, int BT>
-__global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __grid_constant__ RopeArgs r,
-                                                                        const __grid_constant__ QWriteArgs a, int heads,
-                                                                        int n_tab) {
+struct WriteShared {
+  uint32_t red[2][kWriteWarps];
+  int list_n;
+  int2 list[kWriteList];                     // (head of the CTA, row, dim), the scale's inverse
+};
+
+// A CTA's block, of keys or of values (two bodies: values need neither angles nor a
+// second set of codes).
+template <int D, int BT, bool is_v>
+__device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs& a, int heads, int n_tab, int b,
+                                            float2* cs, WriteShared& s) {
   constexpr int LR = D / 8;                  // lanes of a row
   constexpr int RI = 32 / LR;                // rows of a warp at a time
   constexpr int IT = BT / (kWriteWarps * RI) > 0 ? BT / (kWriteWarps * RI) : 1;
-  // [BT][n_tab], (1, 0) past the turned pairs: two pairs next to each other, then those
-  // of the next lane (in pair order the lanes' reads met in the same banks); 8 (1, 0)
-  extern __shared__ float2 cs[];
-  __shared__ uint32_t red[2][kWriteWarps];
-  __shared__ int list_n;
-  __shared__ int2 list[kWriteList];          // (head of the CTA, row, dim), the scale's inverse
-  pdl_trigger();
-  pdl_wait();
   const QCacheArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // keys first: their CTAs take longer
-  const int is_v = blockIdx.z >= gridDim.z / 2, b = blockIdx.z - (is_v ? gridDim.z / 2 : 0);
   const int L = c.seq_lens[b];
   if (L < 0 || static_cast<int64_t>(L) + a.n > static_cast<int64_t>(c.max_pages) * kPg) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) flag_status(c.status, SPEC_DEV_BAD_LENGTH);
@@ -129,7 +126,7 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
     if (threadIdx.x == 0) flag_status(c.status, SPEC_DEV_BAD_PAGE);
     return;
   }
-  if (threadIdx.x == 0) list_n = 0;
+  if (threadIdx.x == 0) s.list_n = 0;
   const bool half = r.layout == SPEC_ROPE_HALF, turns_keys = !is_v && r.n_rot > 0;
   const int hs = r.span / 2;
   float2* none = cs + BT * n_tab;
@@ -168,10 +165,10 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
     uint32_t m = __float_as_uint(x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) red[buf][warp] = m;
+    if (lane == 0) s.red[buf][warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < kWriteWarps; ++v) m = max(m, red[buf][v]);
+    for (int v = 0; v < kWriteWarps; ++v) m = max(m, s.red[buf][v]);
     return m;
   };
 
@@ -291,9 +288,9 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
         const uint2 up = codes(err);
         uint32_t dx = code.x ^ up.x, dy = code.y ^ up.y;
         while (dx | dy) {
-          const int e = (__ffs(dx ? dx : dy) - 1) >> 3, at = atomicAdd(&list_n, 1);
+          const int e = (__ffs(dx ? dx : dy) - 1) >> 3, at = atomicAdd(&s.list_n, 1);
           if (at < kWriteList)
-            list[at] = make_int2((h - h0) << 16 | (t0 + i * RI) << 8 | (d0 + e + (dx ? 0 : 4)), __float_as_int(inv));
+            s.list[at] = make_int2((h - h0) << 16 | (t0 + i * RI) << 8 | (d0 + e + (dx ? 0 : 4)), __float_as_int(inv));
           if (dx) dx &= ~(0xffu << (8 * e));
           else dy &= ~(0xffu << (8 * e));
         }
@@ -305,16 +302,33 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
   // ---- the entries next to a rounding border, over what was stored above (every one
   // of the CTA's, should they be more than the list holds)
   __syncthreads();
-  const bool all = list_n > kWriteList;
-  const int n = all ? (h1 - h0) * (hi - lo) * D : list_n;
+  const bool all = s.list_n > kWriteList;
+  const int n = all ? (h1 - h0) * (hi - lo) * D : s.list_n;
   for (int i = threadIdx.x; i < n; i += kWriteThreads) {
-    const int h = h0 + (all ? i / D / (hi - lo) : static_cast<uint32_t>(list[i].x) >> 16);
-    const int t = all ? lo + i / D % (hi - lo) : list[i].x >> 8 & 0xff, d = all ? i % D : list[i].x & 0xff;
+    const int h = h0 + (all ? i / D / (hi - lo) : static_cast<uint32_t>(s.list[i].x) >> 16);
+    const int t = all ? lo + i / D % (hi - lo) : s.list[i].x >> 8 & 0xff, d = all ? i % D : s.list[i].x & 0xff;
     const int64_t head = static_cast<int64_t>(page) * c.n_kv_heads + h;
-    const float inv = all ? __fdiv_rn(1.f, c.ks[head * (kPg / BT) + (p0 % kPg) / BT]) : __int_as_float(list[i].y);
+    const float inv = all ? __fdiv_rn(1.f, c.ks[head * (kPg / BT) + (p0 % kPg) / BT]) : __int_as_float(s.list[i].y);
     const float v = turned(r, block0 + t * stride + h * D, d, p0 + t);
     c.k[(head * kPg + p0 % kPg + t) * D + d] = static_cast<uint8_t>(e4m3x2(v == v ? v * inv : 0.f, 0.f));
   }
+}
+
+template <int D, int BT>
+__global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __grid_constant__ RopeArgs r,
+                                                                        const __grid_constant__ QWriteArgs a, int heads,
+                                                                        int n_tab) {
+  // [BT][n_tab], (1, 0) past the turned pairs: two pairs next to each other, then those
+  // of the next lane (in pair order the lanes' reads met in the same banks); 8 (1, 0)
+  extern __shared__ float2 cs[];
+  __shared__ WriteShared s;
+  pdl_trigger();
+  pdl_wait();
+  const int B = gridDim.z / 2, z = blockIdx.z;     // keys first: their CTAs take longer
+  if (z < B)
+    write_block<D, BT, false>(r, a, heads, n_tab, z, cs, s);
+  else
+    write_block<D, BT, true>(r, a, heads, n_tab, z - B, cs, s);
 }
 
 // Queries: one warp per head of a row.  q = q_scale * (code0 + code1): the
