@@ -54,10 +54,11 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // hold the block's new rows in registers (a lane 8 dims, IT rows of each warp), find
 // the largest magnitude, settle the scale and store the codes, the next head's rows
 // on their way meanwhile; every row is read once.  The angles of the block's rows are
-// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 75 us, 2.7 TB/s,
-// bound by instruction issue (59% of the slots with 16 warps an SM, which the rows in
-// registers allow): the second set of codes costs 10 us of it, the angles 8.  512
-// threads a CTA, or three CTAs an SM, spill (103 and 119 us).
+// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 68.6 us, 2.9
+// TB/s, bound by instruction issue with 16 warps an SM, which the rows in registers
+// allow: the second set of codes costs 10 us of it, the angles 8.  One body for keys
+// and values 74.8, one for both layouts of keys 70.6; 512 threads a CTA, or three CTAs
+// an SM, spill (103 and 119 us).
 //
 // Codes are those of the exactly turned key.  Keys turn in binary32, off by less
 // than kTurnErr (|x0| + |x1|) magnitude: cosine and sine 1.5 steps and a rounding by
@@ -88,11 +89,12 @@ struct WriteShared {
   int2 list[kWriteList];                     // (head of the CTA, row, dim), the scale's inverse
 };
 
-// A CTA's block, of keys or of values (two bodies: values need neither angles nor a
-// second set of codes).
-template <int D, int BT, bool is_v>
+// A CTA's block: of values (-1), or of keys whose pairs are laid out as LAYOUT (bodies
+// of their own: values need neither angles nor a second set of codes).
+template <int D, int BT, int LAYOUT>
 __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs& a, int heads, int n_tab, int b,
                                             float2* cs, WriteShared& s) {
+  constexpr bool is_v = LAYOUT < 0, half = LAYOUT == SPEC_ROPE_HALF;
   constexpr int LR = D / 8;                  // lanes of a row
   constexpr int RI = 32 / LR;                // rows of a warp at a time
   constexpr int IT = BT / (kWriteWarps * RI) > 0 ? BT / (kWriteWarps * RI) : 1;
@@ -127,7 +129,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
     return;
   }
   if (threadIdx.x == 0) s.list_n = 0;
-  const bool half = r.layout == SPEC_ROPE_HALF, turns_keys = !is_v && r.n_rot > 0;
+  const bool turns_keys = !is_v && r.n_rot > 0;
   const int hs = r.span / 2;
   float2* none = cs + BT * n_tab;
   const int lanes = half ? n_tab / 8 : n_tab / 4;   // that share a row's turned pairs
@@ -325,10 +327,12 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
   pdl_trigger();
   pdl_wait();
   const int B = gridDim.z / 2, z = blockIdx.z;     // keys first: their CTAs take longer
-  if (z < B)
-    write_block<D, BT, false>(r, a, heads, n_tab, z, cs, s);
+  if (z >= B)
+    write_block<D, BT, -1>(r, a, heads, n_tab, z - B, cs, s);
+  else if (r.layout == SPEC_ROPE_HALF)
+    write_block<D, BT, SPEC_ROPE_HALF>(r, a, heads, n_tab, z, cs, s);
   else
-    write_block<D, BT, true>(r, a, heads, n_tab, z - B, cs, s);
+    write_block<D, BT, SPEC_ROPE_INTERLEAVED>(r, a, heads, n_tab, z, cs, s);
 }
 
 // Queries: one warp per head of a row.  q = q_scale * (code0 + code1): the
