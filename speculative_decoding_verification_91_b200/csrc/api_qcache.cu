@@ -109,7 +109,7 @@ struct AttnLayout {
 // the cache's, so that a row's result depends on neither n nor the batch.  A
 // prompt chunk has row blocks enough to fill the GPU, and a split's partial
 // results and its join cost it more than they give (256 rows over 8k of context,
-// 32 / 4 heads: 296 us in three splits, 230 in one, which needs no join): it takes
+// 32 / 4 heads, by 64 rows: 296 us in three splits, 230 in one, which needs no join): it takes
 // the number of splits of the least cost below, up to four items an SM and the
 // kernel's limit of 256 scales an item.
 constexpr int kItemsWanted = 4 * 148;
@@ -118,7 +118,8 @@ int call_split(const spec_qcache* c, int n_q_heads, int64_t B, int n, int max_pa
   if (n <= SPEC_MAX_K + 1) return split;
   const int cap = 256 * c->block_tokens;
   const int64_t rows = (int64_t)(n_q_heads / c->n_kv_heads) * n;
-  const int64_t groups = B * c->n_kv_heads * ((rows + 63) / 64);
+  const int rp = qattn_rows(n, rows);
+  const int64_t groups = B * c->n_kv_heads * ((rows + rp - 1) / rp);
   const int64_t most = (kItemsWanted + groups - 1) / groups, T = (int64_t)max_pages * SPEC_PAGE_SIZE;
   int64_t best = 0, least = INT64_MAX;
   for (int64_t w = 1; w <= most; ++w) {
@@ -178,7 +179,7 @@ size_t attn_bytes(const spec_qcache* c, int n_q_heads, int B, int n, int max_pag
     if (!attn_layout(c, n_q_heads, B, SPEC_MAX_K + 1, max_pages, window, &v)) return 0;
     const uint64_t rows = (uint64_t)B * n * n_q_heads, blocks = rows / 64 + (uint64_t)B * c->n_kv_heads;
     const uint64_t cap = ((uint64_t)max_pages * SPEC_PAGE_SIZE + 4095) / 4096;
-    const uint64_t slots = 64 * (kItemsWanted + 2 * blocks) + rows * (cap + 1);
+    const uint64_t slots = 128 * (kItemsWanted + 2 * blocks) + rows * (cap + 1);
     const size_t most = s.part_o + slots * ((size_t)c->head_dim * 4 + 8) + 512;
     total = most > v.total ? most : v.total;
   }

@@ -9,7 +9,7 @@
 // held in two e4m3 codes whose sum keeps 8 bits: queries q = c0 + c1 (from the
 // query kernel; in TMEM; two MMA passes into one accumulator) and weights p = w0 +
 // w1 / 16 (w1 the rounding error of w0, other rows of the same M tile, so one
-// pass gives both sums, in lanes 16 apart of the accumulator).
+// pass gives both sums, in lanes RP / 4 apart of the accumulator).
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
@@ -33,16 +33,20 @@
 //              (p v_scale <= 2^kLazy), so blocks of any scale share one
 //              accumulator; the sum of p is kept in binary32.
 //
-// Per block of 128 keys (D = 256), in SM clocks: the scores' MMAs 1024, P V 512, a
-// softmax warp 1650 with RP = 32 and 2350 with RP = 64 (exponentials and codes 930,
-// the largest score 250, the store of P 270, the rest latency between them), DRAM
-// 2840 with every SM at work.  So long items of few rows run at the pace of DRAM
-// (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 425 us, 5.4 TB/s, the clock down
-// to 1.45 GHz at the power limit), prompt chunks at that of the softmax (256 rows
-// over 8k, 32 / 4 heads, 2 sequences: 230 us, tensor pipe 54% busy), and calls of
-// some items a CTA also pay for the unequal shares of whole splits.  Not kept: 16
-// softmax warps, a vote after the exponentials instead of before (3% slower), a
-// larger kLazy (1 to 4% faster, coarser small weights).
+// Per block of 128 keys (D = 256), in SM clocks: the scores' MMAs 1024, P V 512 (1024
+// with RP = 128), a softmax warp 1650 with RP = 32, 2350 with 64 (exponentials and
+// codes 930, the largest score 250, the store of P 270, the rest latency between
+// them) and 4200 with 128, DRAM 2840 with every SM at work.  So long items of few rows
+// run at the pace of DRAM (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 425 us, 5.4
+// TB/s, the clock down to 1.45 GHz at the power limit), prompt chunks at that of the
+// softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 191 us; blocks of 64 rows 225),
+// and calls of some items a CTA also pay for the unequal shares of whole splits.  Not
+// kept: 16 softmax warps, a vote after the exponentials instead of before (3%
+// slower), a larger kLazy (1 to 4% faster, coarser small weights).
+//
+// RP = 128 (prompt chunks) has no lanes left for w1's rows: w1 is not scaled, and its
+// tile's product goes into the same accumulator.  Weights are then held to 2^-15 of the
+// reference instead of 2^-19.
 //
 // Value rows of keys outside the item's range or on pages that were not loaded
 // are zeroed in shared memory before P V, so stale slots (NaN codes among them)
@@ -72,7 +76,7 @@ constexpr int kFirstSoft = 4;
 constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
 constexpr uint32_t kSmemMax = 227u * 1024u;
 constexpr int kItems = 4;                  // items described ahead in shared memory
-constexpr uint32_t kTail = 16896;
+constexpr uint32_t kTail = 17408;
 constexpr uint32_t kPBytes = 128 * kBlk;
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
 constexpr int kMaxPg = 256;                // its pages: 16384 keys / 64
@@ -135,12 +139,13 @@ __device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn) {
   return (1u << 4) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int D>
+template <int D, int RP>
 struct Cfg {
   static constexpr uint32_t kUnitBytes = kBlk * D;              // one block's keys or values
   static constexpr int kPBufs = D == 128 ? 2 : 1;
-  static constexpr int kUnits = D == 128 ? 11 : 6;
-  static constexpr uint32_t kOffRing = kPBufs * kPBytes;
+  static constexpr int kUnits = D == 128 ? (RP == 128 ? 9 : 11) : RP == 128 ? 5 : 6;
+  static constexpr uint32_t kPTile = RP == 128 ? 2 * kPBytes : kPBytes;   // both codes' rows in one tile, or a tile each
+  static constexpr uint32_t kOffRing = kPBufs * kPTile;
   static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnitBytes;
   static constexpr uint32_t kSmem = 1024 + kOffTail + kTail;
   static_assert(kSmem <= kSmemMax, "shared memory");
@@ -242,7 +247,7 @@ template <int D, int RP>
 __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constant__ CUtensorMap tk,
                                                             const __grid_constant__ CUtensorMap tv,
                                                             const __grid_constant__ QAttnArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, RP>;
   constexpr int NU = C::kUnits, PB = C::kPBufs, SB = C::kSBufs, ATOMS = D / 128;
   constexpr uint32_t kAtom = kBlk * 128;
   extern __shared__ uint8_t smem_raw[];
@@ -267,9 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   Item* items = reinterpret_cast<Item*>(tail + 512);       // [kItems]
   float* red = reinterpret_cast<float*>(tail + 1024);      // [threads of a row][rows]
   float* alpha_s = red + 256;                              // [rows]
-  float* l_s = alpha_s + 64;                               // [16 keys of a block][rows]: sums of p
+  float* l_s = alpha_s + 128;                              // [16 keys of a block][rows]: sums of p
   float* bad_s = l_s + 512;                                // [rows]
-  float* ks_s = reinterpret_cast<float*>(tail + 4608);     // [kItems][kMaxScales]
+  float* ks_s = reinterpret_cast<float*>(tail + 5120);     // [kItems][kMaxScales]
   float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
   int* pg_s = reinterpret_cast<int*>(vs_s + kItems * kMaxScales);   // [kItems][kMaxPg]; < 0: not there
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -428,11 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           if (!ok) break;
           tc_fence_after();
           const uint32_t v_addr = smem_u32(ring + s * C::kUnitBytes);
-          const uint32_t p_addr = smem_u32(pbuf + (g % PB) * kPBytes);
+          const uint32_t p_addr = smem_u32(pbuf + (g % PB) * C::kPTile);
 #pragma unroll
-          for (int kk = 0; kk < kBlk / 32; ++kk)
-            umma_e4m3(tmem, sw128_desc(p_addr + kk * 32), sw128_desc_mn(v_addr + kk * 4096, kAtom), id_pv,
-                      (j > 0 || kk > 0) ? 1u : 0u);
+          for (uint32_t t = 0; t < C::kPTile; t += kPBytes)
+#pragma unroll
+            for (int kk = 0; kk < kBlk / 32; ++kk)
+              umma_e4m3(tmem, sw128_desc(p_addr + t + kk * 32), sw128_desc_mn(v_addr + kk * 4096, kAtom), id_pv,
+                        (j > 0 || kk > 0 || t > 0) ? 1u : 0u);
           umma_commit(&pv_done[g & 1]);
           umma_commit(&u_empty[s]);
           s += 2;
@@ -582,12 +589,13 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     constexpr int KW = RP / 2;                 // keys of a block a thread takes
     constexpr int NG = kBlk / KW;              // threads of a row
     const int quad = warp & 3, cg = (warp - kFirstSoft) >> 2;     // TMEM lane quadrant; first or second half of its keys
-    const int rh = RP == 64 ? quad & 1 : 0;                       // row half: rows 32 rh + lane
-    const int grp = (RP == 64 ? quad >> 1 : quad) * 2 + cg;       // keys KW grp .. of the block
+    const int rh = RP == 128 ? quad : RP == 64 ? quad & 1 : 0;    // rows 32 rh + lane
+    const int grp = (RP == 128 ? 0 : RP == 64 ? quad >> 1 : quad) * 2 + cg;   // keys KW grp .. of the block
     const int row = rh * 32 + lane;
     const int st = (warp - kFirstSoft) * 32 + lane;               // 0..255
     // Rows of P and of the output: row r in quadrant r / RQ, lane r % RQ for w0,
-    // RQ + r % RQ for w1.  The row of this thread's lane:
+    // RQ + r % RQ for w1 (128 rows: the same lane of a second tile).  The row of this
+    // thread's lane:
     constexpr int RQ = RP / 4;
     const int o_row = quad * RQ + lane % RQ;
     const int p_row = (row / RQ) * 32 + row % RQ;
@@ -643,14 +651,15 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     };
     // rows of P that no query row owns stay zero (what they held cost power: P V is
     // done for all 128)
-    for (int i = st; i < PB * static_cast<int>(kPBytes) / 16; i += kSoftWarps * 32)
+    for (int i = st; i < PB * static_cast<int>(C::kPTile) / 16; i += kSoftWarps * 32)
       reinterpret_cast<uint4*>(pbuf)[i] = make_uint4(0, 0, 0, 0);
     named_bar(1, kSoftWarps * 32);
     pdl_wait();
     bool have_item = take(0);
     int item = 0;
-    constexpr int NE = KW / 16;                       // 16-key groups of a thread (one scale each, and one sum)
-    float l_was[NE] = {}, m_was = 0.f;                // of the item before
+    constexpr int NE = KW / 16;                       // 16-key groups of a thread (one scale each)
+    constexpr int NL = RP == 128 ? 1 : NE;            // sums of p: by 16 keys where rows must not depend on RP
+    float l_was[NL] = {}, m_was = 0.f;                // of the item before
     bool bad_was = false;
     // Ends the item before: (m, l) and o = (o0 + o1 / 16) / kUnit.  Loads of 16
     // lanes leave w0's and w1's sums of a row and a column in one thread (rows lane
@@ -659,14 +668,14 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const Item& x = items[(item - 1) % kItems];
       wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
 #pragma unroll
-      for (int u = 0; u < NE; ++u) l_r[(grp * NE + u) * RP + lane] = l_was[u];
+      for (int u = 0; u < NL; ++u) l_r[(grp * NL + u) * RP + lane] = l_was[u];
       if (grp == 0) bad_s[row] = bad_was ? 1.f : 0.f;
       named_bar(1, kSoft);
       tc_fence_after();
       if (grp == 0 && row < x.nrows && a.n_splits > 1 && !*fail) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < NG * NE; ++e) sum += l_r[e * RP + lane];
+        for (int e = 0; e < NG * NL; ++e) sum += l_r[e * RP + lane];
         __stcg(&a.part_ml[x.slot + row], make_float2(m_was, sum));
       }
       if (quad * RQ < x.nrows) {
@@ -685,28 +694,29 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             dst[i] = a.out + ((x.out0 + pos) * (a.c.n_kv_heads * a.G) + x.h * a.G + (x.r0 + r - pos * a.G)) * D + lane % 4 * 2;
             sum[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < NG * NE; ++e) sum[i] += l_s[e * RP + r];
+            for (int e = 0; e < NG * NL; ++e) sum[i] += l_s[e * RP + r];
             if (bad_s[r] != 0.f) sum[i] = __int_as_float(0x7fffffff);    // a NaN query
           }
         }
-        // 64 columns of eight rows at a time, or 32 of 16
+        // 64 columns of eight rows at a time, or 32 of 16 or (w0 and w1 summed already) 32
         auto readout = [&](auto direct) {
-          constexpr int NC = 64 / NR, NK = NC / 8;
+          constexpr int NC = NR == 1 ? 64 : 32, NK = NC / 8, NO = NR == 1 ? 1 : 2;
 #pragma unroll 1
           for (int c0 = cg * (D / 2); c0 < (cg + 1) * (D / 2); c0 += NC) {
-            uint32_t o[NR][NC / 2];
+            uint32_t o[NO][NC / 2];
 #pragma unroll
-            for (int i = 0; i < NR; ++i) tmem_ld16x256(t_lane + (static_cast<uint32_t>(16 * i) << 16) + c0, o[i]);
+            for (int i = 0; i < NO; ++i) tmem_ld16x256(t_lane + (static_cast<uint32_t>(16 * i) << 16) + c0, o[i]);
 #pragma unroll
-            for (int i = 0; i < NR; ++i) tmem_ld_wait_for(o[i]);
+            for (int i = 0; i < NO; ++i) tmem_ld_wait_for(o[i]);
             float2 y[NR][NK];
 #pragma unroll
             for (int k = 0; k < NK; ++k)
 #pragma unroll
               for (int i = 0; i < NR; ++i) {
-                const int e0 = 4 * k + 2 * i, e1 = NR == 2 ? e0 : 4 * k + 2;
+                const int e0 = NR == 4 ? 0 : 4 * k + 2 * i, e1 = NR == 1 ? 4 * k + 2 : e0;
                 const auto sum_of = [&](int z) {
-                  return fmaf(__uint_as_float(o[NR - 1][e1 + z]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0 + z]) * (1.f / kUnit));
+                  if (NR == 4) return __uint_as_float(o[NO > 1 ? i >> 1 : 0][4 * k + 2 * (i & 1) + z]) * (1.f / kUnit);
+                  return fmaf(__uint_as_float(o[NO - 1][e1 + z]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0 + z]) * (1.f / kUnit));
                 };
                 y[i][k] = make_float2(sum_of(0), sum_of(1));
               }
@@ -750,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       const float* ks = ks_s + (item % kItems) * kMaxScales;
       const float* vs = vs_s + (item % kItems) * kMaxScales;
       if (more) wait(&sc_full[item % kItems], (item / kItems) & 1);
-      float mref = kNoKey, l[NE] = {};
+      float mref = kNoKey, l[NL] = {};
       for (int j = 0; j < nb; ++j, ++g) {
         const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;
         float s[KW], f[NE], vsc[NE], cand = -INFINITY;
@@ -808,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
               al = ex2(mref - bm);              // 0 while the row had no key
               mref = bm;
 #pragma unroll
-              for (int u = 0; u < NE; ++u) l[u] *= al;
+              for (int u = 0; u < NL; ++u) l[u] *= al;
             }
             if (j > 0) {
               // the running sums of the rows that moved (all earlier P V done)
@@ -840,14 +850,15 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             for (int c = 0; c < KW; c += 2) {
               const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
               const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
-              l[c >> 4] += p0;
-              l[c >> 4] += p1;
+              l[NL > 1 ? c >> 4 : 0] += p0;
+              l[NL > 1 ? c >> 4 : 0] += p1;
               const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
               uint16_t c0, c1;
               uint32_t back;
               asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
               asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c0));
-              const __half2 rest = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLow));
+              __half2 rest = __hsub2(x, *reinterpret_cast<const __half2*>(&back));
+              if (RP < 128) rest = __hmul2(rest, __float2half2_rn(kLow));
               asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
               if ((c & 2) == 0) {
                 w0[c >> 2] = c0;
@@ -864,12 +875,12 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         // the P buffer was last read by P V of block g - PB
         if (g >= PB) wait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1);
         if (mine) {
-          uint8_t* pp = pbuf + (g % PB) * kPBytes;
+          uint8_t* pp = pbuf + (g % PB) * C::kPTile;
 #pragma unroll
           for (int u = 0; u < NE; ++u) {
             *reinterpret_cast<uint4*>(pp + swz128(p_row, NE * grp + u)) =
                 make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
-            *reinterpret_cast<uint4*>(pp + swz128(p_row + RQ, NE * grp + u)) =
+            *reinterpret_cast<uint4*>(pp + (RP == 128 ? kPBytes + swz128(p_row, NE * grp + u) : swz128(p_row + RQ, NE * grp + u))) =
                 make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
           }
         }
@@ -894,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       }
       if (!more) break;
 #pragma unroll
-      for (int u = 0; u < NE; ++u) l_was[u] = l[u];
+      for (int u = 0; u < NL; ++u) l_was[u] = l[u];
       m_was = mref;
       bad_was = bad_q;
       have_item = take(item + 1);
@@ -1070,22 +1081,23 @@ cudaError_t launch_one(int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                        const QAttnArgs& a, cudaStream_t st) {
   auto kern = qattn_kernel<D, RP>;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(kern, Cfg<D>::kSmem, allowed);
+  const cudaError_t e = allow_smem(kern, Cfg<D, RP>::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, tk, tv, a);
+  return launch_k(kern, dim3(grid), dim3(kThreads), Cfg<D, RP>::kSmem, st, tk, tv, a);
 }
 
 template <int D>
 cudaError_t launch_dim(int rp, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                        const QAttnArgs& a, cudaStream_t st) {
   if (rp == 32) return launch_one<D, 32>(grid, tk, tv, a, st);
+  if (rp == 128) return launch_one<D, 128>(grid, tk, tv, a, st);
   return launch_one<D, 64>(grid, tk, tv, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_qcache_attn(const QAttnArgs& a, cudaStream_t st) {
-  const int D = a.c.dim, rp = a.rows <= 32 ? 32 : 64;
+  const int D = a.c.dim, rp = qattn_rows(a.n, a.rows);
   const uint64_t rows = static_cast<uint64_t>(a.c.num_pages) * a.c.n_kv_heads * kPg;
   CUtensorMap tk, tv;
   if (!make_tmap_u8_2d(&tk, a.c.k, rows, D, kPg, 128) || !make_tmap_u8_2d(&tv, a.c.v, rows, D, kPg, 128))
