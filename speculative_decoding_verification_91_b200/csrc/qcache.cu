@@ -341,9 +341,9 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
 // bf16's 2^-9 on average, and both factors of the score product are e4m3.  A
 // row with an infinity or NaN gets a NaN scale, which makes its result NaN.
 // A CTA takes a row of a sequence and every blockIdx.y-th four of its heads, a warp a head (4 or
-// 8 dims a lane): the row's angles once for all of them (each warp forming its own took 41 us
-// instead of 16 for 512 rows of 32 heads), the first head asked for before.  Few rows: 4.5 us,
-// most of it under the split kernel's start.
+// 8 dims a lane, one load): the row's angles once for all of them (each warp forming its own
+// took 41 us for 512 rows of 32 heads, 12.5 now), the first head asked for before.  Few rows: 4.5
+// us, most of it under the split kernel's start.
 template <int D>
 __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant__ RopeArgs r,
                                                            const __grid_constant__ QAttnArgs a) {
@@ -371,13 +371,28 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
     pair[e] = j;
     partner[e] = w;
   }
-  float own[P], with[P];
+  // the lane's own dims, and their partners: next to them, whole lanes away, or (half
+  // pairs of an odd distance) anywhere
+  const bool half_pairs = r.layout == SPEC_ROPE_HALF, far = half_pairs && half % P != 0;
+  const int from = !half_pairs || far || lane * P >= r.span ? lane : lane * P < half ? lane + half / P : lane - half / P;
+  uint32_t raw[P / 2];
+  uint16_t other[P];
   auto load = [&](int hq) {
     const uint16_t* p = a.q + bi * a.q_row + static_cast<int64_t>(hq) * D;
+    if (P == 8) {
+      const uint4 z = *reinterpret_cast<const uint4*>(p + lane * P);
+      raw[0] = z.x;
+      raw[1] = z.y;
+      raw[P / 2 - 2] = z.z;
+      raw[P / 2 - 1] = z.w;
+    } else {
+      const uint2 z = *reinterpret_cast<const uint2*>(p + lane * P);
+      raw[0] = z.x;
+      raw[1] = z.y;
+    }
+    if (far) {
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      own[e] = bf16_to_f32(p[lane * P + e]);
-      with[e] = bf16_to_f32(p[partner[e]]);
+      for (int e = 0; e < P; ++e) other[e] = p[partner[e]];
     }
   };
   int hq = blockIdx.y * 4 + (threadIdx.x >> 5);
@@ -391,8 +406,16 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
   __syncthreads();
   for (; hq < n_heads; hq += gridDim.y * 4) {
     if (hq >= static_cast<int>(gridDim.y) * 4) load(hq);
-    float amax = 0.f;
+    float own[P], with[P], amax = 0.f;
     bool bad = false;
+#pragma unroll
+    for (int e = 0; e < P; e += 2) {
+      const uint32_t o = __shfl_sync(0xffffffffu, raw[e / 2], from);
+      own[e] = __uint_as_float(raw[e / 2] << 16);
+      own[e + 1] = __uint_as_float(raw[e / 2] & 0xffff0000u);
+      with[e] = far ? bf16_to_f32(other[e]) : half_pairs ? __uint_as_float(o << 16) : own[e + 1];
+      with[e + 1] = far ? bf16_to_f32(other[e + 1]) : half_pairs ? __uint_as_float(o & 0xffff0000u) : own[e];
+    }
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       if (pair[e] >= 0) {
@@ -420,12 +443,13 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
       c0[e / 4] = e % 4 ? c0[e / 4] | x << 16 : x;
       c1[e / 4] = e % 4 ? c1[e / 4] | y << 16 : y;
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.q_codes + row * D + lane * P);
-    uint32_t* dst1 = reinterpret_cast<uint32_t*>(a.q_codes + plane + row * D + lane * P);
-#pragma unroll
-    for (int e = 0; e < P / 4; ++e) {
-      dst[e] = c0[e];
-      dst1[e] = c1[e];
+    uint8_t* dst = a.q_codes + row * D + lane * P;
+    if (P == 8) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(c0[0], c0[P / 4 - 1]);
+      *reinterpret_cast<uint2*>(dst + plane) = make_uint2(c1[0], c1[P / 4 - 1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(dst) = c0[0];
+      *reinterpret_cast<uint32_t*>(dst + plane) = c1[0];
     }
     if (lane == 0) a.q_scale[row] = bad ? __int_as_float(0x7fffffff) : pow2f(e2);
     // where results are written by the attention kernel itself, a sequence that
@@ -467,9 +491,11 @@ cudaError_t launch_qcache_write(const RopeArgs& r, const QWriteArgs& a, cudaStre
 }
 
 cudaError_t launch_qcache_queries(const RopeArgs& r, const QAttnArgs& a, cudaStream_t st) {
-  // few rows: a warp for every head; many: the angles of a row formed once
+  // few rows: a warp for every head; many: up to eight CTAs an SM, so that the angles of
+  // a row are formed once or twice (512 rows of 32 heads, the whole prompt chunk: 189 us
+  // with one CTA a row, 182 with two, 187 with eight)
   const int n_heads = a.c.n_kv_heads * a.G, rows = a.B * a.n;
-  const dim3 grid(rows, rows >= 148 ? 1 : (n_heads + 3) / 4);
+  const dim3 grid(rows, std::min((n_heads + 3) / 4, std::max(1, 8 * 148 / rows)));
   return a.c.dim == 256 ? launch_k(qcache_query_kernel<256>, grid, dim3(128), 0, st, r, a)
                         : launch_k(qcache_query_kernel<128>, grid, dim3(128), 0, st, r, a);
 }
