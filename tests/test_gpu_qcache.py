@@ -287,6 +287,43 @@ def test_write_of_keys_next_to_rounding_borders(ties, layout):
     c.same()
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("side", [-1, 0, 1])
+def test_write_of_blocks_whose_scale_turns_on_one_entry(layout, side):
+    """The largest key within 10^-7 of 448 x a power of two: just below (the smaller scale), on it
+    (a dim that passes through), or just above (the larger one)."""
+    H, D, n, block, n_rot = 3, 128, 40, 16, 32
+    c = Cache(6, [20, 0], n, H, D, block)
+    c.fill()
+    freq = Q.rope_frequencies(128, n_rot)
+    x = torch.from_numpy(c.rng.normal(size=(2, n, H, D)) * 0.2).clamp(-0.8, 0.8).to(torch.bfloat16)
+    if side == 0:
+        x[..., 60] = 1.75                               # neither turned half nor pair
+    else:
+        # the pair of bf16 numbers that turns closest to 1.75 from that side, at each position and pair
+        one = (1 + np.arange(128) / 128)
+        v = np.concatenate([one / 2, one])
+        for b, L in enumerate(c.lens):
+            for i in range(0, n, 3):
+                j = int(c.rng.integers(0, n_rot))
+                angle = (L + i) * freq[j]
+                y = v[:, None] * math.cos(angle) - np.concatenate([-v, v])[None] * math.sin(angle)
+                off = (np.abs(y) - 1.75) * side
+                other = v[:, None] * math.sin(angle) + np.concatenate([-v, v])[None] * math.cos(angle)
+                off[(off <= 0) | (np.abs(other) > 1.7)] = np.inf
+                a, w = np.unravel_index(np.argmin(off), off.shape)
+                d0, d1 = (j, j + 64) if layout == "half" else (2 * j, 2 * j + 1)
+                x[b, i, i % H, d0], x[b, i, i % H, d1] = float(v[a]), float(np.concatenate([-v, v])[w])
+    k, v = x.cuda(), c.rows(n, H)
+    for b, L in enumerate(c.lens):
+        Q.append(c.k, c.ks, block, c.table[b], L, turned(k[b], L, freq, layout, 128))
+        Q.append(c.v, c.vs, block, c.table[b], L, v[b].double().cpu().numpy())
+    ws = workspace(B.spec_qcache_write_workspace_bytes(c.desc, 2, n))
+    B.spec_qcache_write(c.desc, rope_config(128, n_rot, layout), c.d["table"], c.max_pages, c.d["lens"], 2, n, k, H * D,
+                        v, H * D, ws, ws.numel())
+    c.same()
+
+
 # ----------------------------------------------------------------- attention
 
 def attention_bound(out, spread, mass, tail, rows=1):
