@@ -39,7 +39,7 @@
 // them) and 4200 with 128, DRAM 2840 with every SM at work.  So long items of few rows
 // run at the pace of DRAM (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 425 us, 5.4
 // TB/s, the clock down to 1.45 GHz at the power limit), prompt chunks at that of the
-// softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 191 us; blocks of 64 rows 225),
+// softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 182 to 193 us; blocks of 64 rows 225),
 // and calls of some items a CTA also pay for the unequal shares of whole splits.  Not
 // kept: 16 softmax warps, a vote after the exponentials instead of before (3%
 // slower), a larger kLazy (1 to 4% faster, coarser small weights).

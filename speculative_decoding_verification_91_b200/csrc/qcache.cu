@@ -54,7 +54,7 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // hold the block's new rows in registers (a lane 8 dims, IT rows of each warp), find
 // the largest magnitude, settle the scale and store the codes, the next head's rows
 // on their way meanwhile; every row is read once.  The angles of the block's rows are
-// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 68.6 us, 2.9
+// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 67.5 us, 3.0
 // TB/s, bound by instruction issue with 16 warps an SM, which the rows in registers
 // allow: the second set of codes costs 10 us of it, the angles 8.  One body for keys
 // and values 74.8, one for both layouts of keys 70.6; 512 threads a CTA, or three CTAs
@@ -65,8 +65,8 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // the magnitude each, the product, the sum, 4.5 x 2^-24.  Where rounding that much
 // lower and higher (by a lane's largest own and partner's magnitude) gives two codes
 // (3 in 10^4) the entry is formed again in binary64, all of a CTA's together at its
-// end.  Blocks with infinities or NaN, blocks whose scale would turn on that error,
-// and half pairs whose distance is no multiple of 8 take binary64 throughout.  (All
+// end.  Blocks with infinities or NaN and half pairs
+// whose distance is no multiple of 8 take binary64 throughout.  (All
 // of it in binary64, with each head its own angles, took 545 us for 64 x 256 tokens
 // of 8 heads; entries formed again where they were found, 160-230; a warp a head that
 // reads its rows twice, 135.)
@@ -224,9 +224,6 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
             (fmaxf(__low2float(top), __high2float(top)) + fmaxf(__low2float(with), __high2float(with)));
     }
     uint32_t m = block_max(plain ? amax : INFINITY, h & 1);
-    // the scale turns at 1.75 x 2^x: a turned magnitude is within 2 kTurnErr,
-    // 8 steps of binary32, of it
-    const bool exact = m >= 0x7f800000u || (turns_keys && abs(static_cast<int>(m & 0x7fffffu) - 0x600000) <= 16);
     const uint16_t* head0 = block0 + h * D;
     // the entries one by one, in binary64
     auto entries = [&](auto&& f) {
@@ -239,7 +236,28 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
           f(t, e, is_v ? bf16_to_f32(head0[t * stride + d0 + e]) : turned(r, head0 + t * stride, d0 + e, p0 + t));
       }
     };
-    if (exact) {                             // (uniform in the CTA)
+    const bool exact = m >= 0x7f800000u;     // (uniform in the CTA)
+    // the scale turns at 1.75 x 2^x: a turned magnitude is within 2 kTurnErr of the
+    // largest, 8 steps of binary32, of itself.  Next to that the largest is found in
+    // binary64, among the entries that may be above (every block with one in a hundred
+    // amaxes of bf16 comes here; all entries in binary64 took 40 us)
+    if (turns_keys && !exact && abs(static_cast<int>(m & 0x7fffffu) - 0x600000) <= 16) {
+      const uint32_t least = ((m & 0x7f800000u) | 0x600000u) - 16;
+      uint64_t may = 0;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((__float_as_uint(y[i][e]) & 0x7fffffffu) >= least) may |= 1ull << (8 * i + e);
+      float top = 0.f;
+      for (; may; may &= may - 1) {
+        const int k = __ffsll(static_cast<long long>(may)) - 1, t = t0 + k / 8 * RI;
+        top = fmaxf(top, fabsf(turned(r, head0 + t * stride, d0 + k % 8, p0 + t)));
+      }
+      __syncthreads();
+      m = block_max(top, h & 1);
+    }
+    if (exact) {
       bool bad = false;
       amax = 0.f;
       entries([&](int, int, float v) {
