@@ -116,3 +116,24 @@ def test_workspace_sizes(lib):
     assert B.spec_qcache_attn_workspace_bytes(c, 7, 8, 5, 100) == 0
     assert B.spec_qcache_attn_workspace_bytes(c, 8, 8, 257, 100) == 0
     assert B.spec_qcache_attn_workspace_bytes(cache(head_dim=96), 8, 8, 5, 100) == 0
+
+
+def test_counts_past_32_bits_are_refused(lib):
+    """Key blocks of all row blocks, and rows by query heads, are counted in 32 bits: sizes past that
+    have no workspace; large ones within it do, whatever the window leaves of them."""
+    c = cache()
+    assert B.spec_qcache_attn_workspace_bytes(c, 8, 64, 17, 1 << 17, 64) > 4096
+    assert B.spec_qcache_attn_workspace_bytes(c, 8, 65535, 17, 1 << 17, 64) == 0
+    # G query heads a KV head (two of them): 17 G rows by G, below 2^32 up to G = 15894
+    assert B.spec_qcache_attn_workspace_bytes(c, 2 * 15894, 1, 17, 100) > 4096
+    assert B.spec_qcache_attn_workspace_bytes(c, 2 * 15895, 1, 17, 100) == 0
+
+
+@pytest.mark.parametrize("n", [17, 100, 256])
+def test_a_workspace_serves_smaller_calls(lib, n):
+    """The size for the largest call covers smaller ones, which take the cache's own, shorter splits."""
+    for c in (cache(), cache(split_tokens=128), cache(block_tokens=16)):
+        for heads in (8, 64):
+            most = B.spec_qcache_attn_workspace_bytes(c, heads, 8, n, 400)
+            for batch, rows, pages in ((8, 17, 400), (8, 1, 400), (1, 17, 400), (3, 5, 37), (1, 1, 1)):
+                assert B.spec_qcache_attn_workspace_bytes(c, heads, batch, rows, pages) <= most
