@@ -118,6 +118,19 @@ __device__ __forceinline__ void turn_piece(Piece<T>& a, Piece<T>& b, const float
   }
 }
 
+// The first `turning` pairs of a piece.
+template <typename T, bool HALF>
+__device__ __forceinline__ void turn_some(Piece<T>& a, Piece<T>& b, const float2 (&c)[(HALF ? 16 : 8) / sizeof(T)], int turning) {
+  constexpr int PP = (HALF ? 16 : 8) / sizeof(T);
+  if (turning == PP) {
+    turn_piece<T, HALF>(a, b, c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < PP; ++e)
+      if (e < turning) turn(a.e[HALF ? e : 2 * e], HALF ? b.e[HALF ? e : 0] : a.e[HALF ? 0 : 2 * e + 1], c[e]);
+  }
+}
+
 // Positions and (c, s) of the CTA's rows; ends with a barrier.
 __device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, const RopePlan& p, int64_t row0,
                                        float2* cs, int* pos) {
@@ -136,7 +149,8 @@ __device__ __forceinline__ void angles(const RopeArgs& r, const RopeOpArgs& a, c
 
 // A thread keeps its piece (or two opposite ones) of a head, and with it the pairs'
 // frequencies, and goes down the CTA's rows.
-template <typename T, int LAYOUT>
+// ROWS: one head, so the loads of several rows are in flight instead of several heads'.
+template <typename T, int LAYOUT, bool ROWS>
 __global__ void __launch_bounds__(kDirectThreads) rope_direct_kernel(const __grid_constant__ RopeArgs r,
                                                                      const __grid_constant__ RopeOpArgs a,
                                                                      const __grid_constant__ RopePlan p) {
@@ -163,6 +177,39 @@ __global__ void __launch_bounds__(kDirectThreads) rope_direct_kernel(const __gri
   const int64_t first = static_cast<int64_t>(block) * p.side * p.rows + t0, last = min(first + p.side * p.rows, static_cast<int64_t>(a.n_rows));
   const T* src0 = static_cast<const T*>(a.x) + h0 * a.x_head + d;
   T* dst0 = static_cast<T*>(a.out) + h0 * a.out_head + d;
+  if (ROWS) {
+    for (int64_t row = first; row < last; row += B * p.side) {
+      Piece<T> x0[B], x1[HALF ? B : 1];
+      int at[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int64_t rb = row + b * p.side;
+        at[b] = -1;
+        if (rb >= last) continue;
+        at[b] = a.positions[rb];
+        x0[b].v = __ldcs(reinterpret_cast<const uint4*>(src0 + rb * a.x_row));
+        if (HALF && pair) x1[b].v = __ldcs(reinterpret_cast<const uint4*>(src0 + rb * a.x_row + r.span / 2));
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (at[b] < 0) continue;
+        if (turning > 0) {
+          float2 cs[PP];
+#pragma unroll
+          for (int e = 0; e < PP; ++e) {
+            float c, s;
+            rope_turn(at[b], step[e], static_cast<float>(r.magnitude), c, s);
+            cs[e] = make_float2(c, a.inverse ? -s : s);
+          }
+          turn_some<T, HALF>(x0[b], x1[HALF ? b : 0], cs, turning);
+        }
+        T* dst = dst0 + (row + b * p.side) * a.out_row;
+        *reinterpret_cast<uint4*>(dst) = x0[b].v;
+        if (HALF && pair) *reinterpret_cast<uint4*>(dst + r.span / 2) = x1[b].v;
+      }
+    }
+    return;
+  }
   int pos = first < last ? a.positions[first] : -1;
   for (int64_t row = first; row < last; row += p.side) {
     const int at = pos;
@@ -192,13 +239,7 @@ __global__ void __launch_bounds__(kDirectThreads) rope_direct_kernel(const __gri
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         if (h + b >= heads) break;
-        if (turning == PP) {
-          turn_piece<T, HALF>(x0[b], x1[HALF ? b : 0], cs);
-        } else {
-#pragma unroll
-          for (int e = 0; e < PP; ++e)
-            if (e < turning) turn(x0[b].e[HALF ? e : 2 * e], HALF ? x1[HALF ? b : 0].e[e] : x0[b].e[2 * e + 1], cs[e]);
-        }
+        turn_some<T, HALF>(x0[b], x1[HALF ? b : 0], cs, turning);
         *reinterpret_cast<uint4*>(dst + (h + b) * a.out_head) = x0[b].v;
         if (HALF && pair) *reinterpret_cast<uint4*>(dst + (h + b) * a.out_head + r.span / 2) = x1[b].v;
       }
@@ -278,9 +319,12 @@ cudaError_t launch_typed(const RopeArgs& r, const RopeOpArgs& a, cudaStream_t st
     p.by_n = make_div(n);
     const int64_t per = static_cast<int64_t>(p.side) * p.rows, ctas = (a.n_rows + per - 1) / per * p.chunks;
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(ctas));
-    return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF>, grid, dim3(kDirectThreads), 0, st, r, a, p)
-                : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED>, grid, dim3(kDirectThreads), 0, st, r, a, p);
+    const dim3 grid(static_cast<unsigned>(ctas)), block(kDirectThreads);
+    if (a.n_heads == 1)
+      return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF, true>, grid, block, 0, st, r, a, p)
+                  : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED, true>, grid, block, 0, st, r, a, p);
+    return half ? launch_k(rope_direct_kernel<T, SPEC_ROPE_HALF, false>, grid, block, 0, st, r, a, p)
+                : launch_k(rope_direct_kernel<T, SPEC_ROPE_INTERLEAVED, false>, grid, block, 0, st, r, a, p);
   }
   // bytes of a CTA: enough in flight for many rows, spread over the SMs for few
   const int64_t head = static_cast<int64_t>(a.dim) * sizeof(T), total = head * a.n_heads * a.n_rows;
