@@ -93,6 +93,30 @@ def test_rope_strided_in_place_and_transposed(layout, shift):
     assert torch.equal(fused[:, shift + heads * dim:], before[:, shift + heads * dim:])
 
 
+@pytest.mark.parametrize("layout,rows,heads,dim,span,n_rot", [
+    ("half", 150001, 1, 192, 64, 32), ("interleaved", 90001, 1, 192, 64, 27), ("half", 60001, 3, 128, 128, 20)])
+def test_rope_of_many_rows(layout, rows, heads, dim, span, n_rot):
+    """More rows than threads side by side: each thread takes several, with padding rows among them."""
+    rng = np.random.default_rng(rows)
+    freq = Q.rope_frequencies(span, n_rot)
+    x = torch.randn(rows, heads, dim, device="cuda").to(torch.bfloat16)
+    pos = rng.integers(0, 131072, rows).astype(np.int32)
+    pos[rng.integers(0, rows, 50)] = -1
+    pos[-1] = 131071
+    out = torch.full_like(x, 7.0)
+    B.spec_rope(rope_config(span, n_rot, layout), B.SPEC_BF16, x, x.stride(0), x.stride(1), out, out.stride(0),
+                out.stride(1), torch.from_numpy(pos).cuda(), rows, heads, dim)
+    xs, got = x.double().cpu().numpy(), out.double().cpu().numpy()
+    want = Q.rope(xs, pos, freq, layout, span)
+    want[pos < 0] = 7.0
+    assert np.all(np.abs(got - want) <= rope_bound(xs, want, torch.bfloat16, pos, freq, 1.0))
+    inplace = x.clone()
+    B.spec_rope(rope_config(span, n_rot, layout), B.SPEC_BF16, inplace, x.stride(0), x.stride(1), inplace, x.stride(0),
+                x.stride(1), torch.from_numpy(pos).cuda(), rows, heads, dim)
+    there = torch.from_numpy(pos >= 0).cuda()
+    assert torch.equal(inplace[there], out[there]) and torch.equal(inplace[~there], x[~there])
+
+
 def test_rope_passes_infinities_and_nan_of_unturned_dims_and_repeats_a_head():
     """Dims that do not turn are copied whatever they hold; a head read by stride 0 is turned into each."""
     x = torch.ones(2, 1, 16, dtype=torch.float32, device="cuda")
