@@ -527,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
         continue;
       }
       const int q = i % kItems;
-      if (i >= kItems) wait(&it_empty[q], ((i / kItems) - 1) & 1);
+      // (given up: the slot is not touched, the softmax warps may be about to read it)
+      if (i >= kItems && !__all_sync(0xffffffffu, wait(&it_empty[q], ((i / kItems) - 1) & 1))) break;
       if (lane == 0) {
         Item& x = items[q];
         x.h = w.h;
