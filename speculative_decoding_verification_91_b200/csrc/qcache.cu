@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
                                                                         int n_tab) {
   // [BT][n_tab], (1, 0) past the turned pairs: two pairs next to each other, then those
   // of the next lane (in pair order the lanes' reads met in the same banks); 8 (1, 0)
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float2 cs[];
   __shared__ WriteShared s;
   pdl_trigger();
   pdl_wait();

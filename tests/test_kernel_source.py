@@ -21,3 +21,21 @@ def test_waits_for_an_item_s_slot_are_heeded():
     assert len(re.findall(r"wait\(&it_(full|empty)\[", text)) >= 5
     dropped = re.findall(r"[;{})]\s*wait\(&it_(?:full|empty)\[[^;]*;", text)
     assert not dropped, dropped
+
+
+def test_shared_memory_read_in_16_byte_pieces_is_aligned_to_them():
+    """A kernel's dynamic shared memory follows its static one: what is read 16 bytes at a time has to be
+    declared so, aligned by hand, or of a 16-byte type."""
+    seen = 0
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith(".cu"):
+            continue
+        text = source(name)
+        if not re.search(r"reinterpret_cast<(?:const )?(?:u?int4|float4)\*>", text):
+            continue
+        for align, kind, var in re.findall(r"extern __shared__\s+(__align__\(\d+\)\s+)?([\w ]+?)\s+(\w+)\[\]", text):
+            seen += 1
+            by_hand = re.search(r"reinterpret_cast<uintptr_t>\(%s\)\s*\+\s*1023" % var, text)
+            only_small = not re.search(r"float4\*>\([^;]*\b%s\b" % var, text) and kind in ("float2", "unsigned long long")
+            assert align or by_hand or kind == "uint4" or only_small, (name, var)
+    assert seen >= 5
