@@ -9,7 +9,7 @@
 // held in two e4m3 codes whose sum keeps 8 bits: queries q = c0 + c1 (from the
 // query kernel; in TMEM; two MMA passes into one accumulator) and weights p = w0 +
 // w1 / 16 (w1 the rounding error of w0, other rows of the same M tile, so one
-// pass gives both sums, in lanes RP / 4 apart of the accumulator).
+// pass gives both sums, in lanes RP / 4 apart of the accumulator; RP = 128: below).
 //
 // Work item = (sequence, KV head, block of RP query rows, absolute split of
 // split_tokens keys); items are ordered and every CTA (one per SM) takes those
@@ -33,20 +33,25 @@
 //              (p v_scale <= 2^kLazy), so blocks of any scale share one
 //              accumulator; the sum of p is kept in binary32.
 //
-// Per block of 128 keys (D = 256), in SM clocks: the scores' MMAs 1024, P V 512 (1024
+// Per block of 128 keys (D = 256), in SM clocks: the scores' MMAs 1024, P V 512 (1536
 // with RP = 128), a softmax warp 1650 with RP = 32, 2350 with 64 (exponentials and
 // codes 930, the largest score 250, the store of P 270, the rest latency between
-// them) and 4200 with 128, DRAM 2840 with every SM at work.  So long items of few rows
+// them) and 5800 with 128, DRAM 2840 with every SM at work.  So long items of few rows
 // run at the pace of DRAM (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 425 us, 5.4
 // TB/s, the clock down to 1.45 GHz at the power limit), prompt chunks at that of the
-// softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 182 to 193 us; blocks of 64 rows 225),
+// softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 212 us),
 // and calls of some items a CTA also pay for the unequal shares of whole splits.  Not
 // kept: 16 softmax warps, a vote after the exponentials instead of before (3%
 // slower), a larger kLazy (1 to 4% faster, coarser small weights).
 //
-// RP = 128 (prompt chunks) has no lanes left for w1's rows: w1 is not scaled, and its
-// tile's product goes into the same accumulator.  Weights are then held to 2^-15 of the
-// reference instead of 2^-19.
+// RP = 128 (prompt chunks) has no lanes left for w1's rows: its weights are three e5m2
+// codes in tiles of their own, w0 + w1 + w2, summed in one accumulator.  e5m2 is
+// binary16's upper byte, so the first two are masks instead of conversions, and its
+// range holds a weight to 2^-9 of itself down to 2^-18 of the reference, under which an
+// item keeps up to 16384 keys.  (Two e4m3 codes without a scale between them kept
+// weights above 2^-15 only: 182 us for the chunk below instead of 212, but beside a sink
+// of 95 % results were off by 35 to 45 %.  w1 as e5m2 beside an e4m3 w0: 3 % where the
+// others weigh the same.  Blocks of 64 rows: 215 us.)
 //
 // Value rows of keys outside the item's range or on pages that were not loaded
 // are zeroed in shared memory before P V, so stale slots (NaN codes among them)
@@ -80,11 +85,14 @@ constexpr uint32_t kTail = 17408;
 constexpr uint32_t kPBytes = 128 * kBlk;
 constexpr int kMaxScales = 256;            // scales of one item: 4096 keys / 16
 constexpr int kMaxPg = 256;                // its pages: 16384 keys / 64
-// p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448.  A larger
-// kLazy moves the reference less often, a larger kUnit keeps smaller weights
-// (w1's least step is 2^-9 / (kUnit kLow) = 2^-18 of the reference).
+// p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448, with RP = 128
+// 23170 (e5m2 goes to 57344).  A larger kLazy moves the reference less often, a larger
+// kUnit keeps smaller weights: the least steps are 2^-9 / (32 kLow) = 2^-18 and 2^-16 /
+// 2048 = 2^-27 of the reference.  (32 rows' weights in units of 128 and 256, kLazy 1.8
+// and 0.8: 8 sequences 96 -> 107 and 109 us, the references move more often.)
 constexpr float kLazy = 3.5f;
-constexpr float kUnit = 32.f;
+template <int RP>
+constexpr float kUnit = RP == 128 ? 2048.f : 32.f;
 constexpr float kLow = 16.f;               // w1 is stored times 16
 constexpr float kNoKey = -1e30f;           // reference of a row that has seen no key
 
@@ -106,6 +114,15 @@ __device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&v)[16])
 __device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&v)[32]) {
   tmem_ld16x256(taddr, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
   tmem_ld16x256(taddr + 32, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+}
+// Added to the weight of key c of a block before it is coded (RP <= 64): 16 values spread evenly over one least
+// step of w1 around 0, so that weights below that step are dropped or raised to it in shares that sum to what
+// they are.  Rounded to nearest, thousands of small weights beside a dominant one (an attention sink) all went
+// the same way, while the sum of p below the line kept them: results were off by 2 to 8 % (a sink of 99 % beside
+// 4096 keys), now 0.2.  Less than half a step, so a weight of 0 stays 0.
+__device__ __forceinline__ constexpr float spread(int c) {
+  const int turned = (c & 1) << 3 | (c & 2) << 1 | (c & 4) >> 1 | (c & 8) >> 3;   // neighbours far apart
+  return (static_cast<float>(turned) - 7.5f) / 16.f * (0x1p-9f / kLow);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -133,18 +150,19 @@ __device__ __forceinline__ void umma_e4m3_ta(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor, kind::f8f6f4: D binary32, A and B e4m3, M = 128, N = n,
-// A K-major, B K-major or MN-major.
-__device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn) {
-  return (1u << 4) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4: D binary32, A e4m3 or e5m2, B e4m3, M = 128,
+// N = n, A K-major, B K-major or MN-major.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_mn, bool a_e5m2) {
+  return (1u << 4) | (a_e5m2 ? (1u << 7) : 0u) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
 }
 
 template <int D, int RP>
 struct Cfg {
   static constexpr uint32_t kUnitBytes = kBlk * D;              // one block's keys or values
   static constexpr int kPBufs = D == 128 ? 2 : 1;
-  static constexpr int kUnits = D == 128 ? (RP == 128 ? 9 : 11) : RP == 128 ? 5 : 6;
-  static constexpr uint32_t kPTile = RP == 128 ? 2 * kPBytes : kPBytes;   // both codes' rows in one tile, or a tile each
+  static constexpr int kUnits = D == 128 ? (RP == 128 ? 7 : 11) : RP == 128 ? 5 : 6;
+  static constexpr uint32_t kPTile = RP == 128 ? 3 * kPBytes : kPBytes;   // both codes' rows in one tile, or three tiles
   static constexpr uint32_t kOffRing = kPBufs * kPTile;
   static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnitBytes;
   static constexpr uint32_t kSmem = 1024 + kOffTail + kTail;
@@ -388,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     // ------------------------------------------------------------- scores
     ready();
     if (lane == 0) {
-      const uint32_t id_qk = idesc_e4m3(kBlk, false);
+      const uint32_t id_qk = idesc_e4m3(kBlk, false, false);
       int s = 0, su = 0, g = 0, nq = 0;     // ring slot and its round, block, query groups begun
       for (int i = 0;; ++i) {
         if (!wait(&it_full[i % kItems], (i / kItems) & 1)) break;
@@ -422,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     // (a thread of its own: one thread that issued both spent 600 clocks from
     // the last MMA of one product to the first of the other)
     if (lane == 0) {
-      const uint32_t id_pv = idesc_e4m3(D, true);
+      const uint32_t id_pv = idesc_e4m3(D, true, RP == 128);
       int s = 2, su = 0, g = 0;
       for (int i = 0;; ++i) {
         if (!wait(&it_full[i % kItems], (i / kItems) & 1)) break;
@@ -658,6 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     pdl_wait();
     bool have_item = take(0);
     int item = 0;
+    // a thread's keys are coded and stored in parts: registers (RP = 128 all at once: 231 us for the chunk, two parts 218)
+    constexpr int PARTS = RP == 128 ? 4 : 1, KP = KW / PARTS;
     constexpr int NE = KW / 16;                       // 16-key groups of a thread (one scale each)
     constexpr int NL = RP == 128 ? 1 : NE;            // sums of p: by 16 keys where rows must not depend on RP
     float l_was[NL] = {}, m_was = 0.f;                // of the item before
@@ -716,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
               for (int i = 0; i < NR; ++i) {
                 const int e0 = NR == 4 ? 0 : 4 * k + 2 * i, e1 = NR == 1 ? 4 * k + 2 : e0;
                 const auto sum_of = [&](int z) {
-                  if (NR == 4) return __uint_as_float(o[NO > 1 ? i >> 1 : 0][4 * k + 2 * (i & 1) + z]) * (1.f / kUnit);
-                  return fmaf(__uint_as_float(o[NO - 1][e1 + z]), 1.f / (kUnit * kLow), __uint_as_float(o[0][e0 + z]) * (1.f / kUnit));
+                  if (NR == 4) return __uint_as_float(o[NO > 1 ? i >> 1 : 0][4 * k + 2 * (i & 1) + z]) * (1.f / kUnit<RP>);
+                  return fmaf(__uint_as_float(o[NO - 1][e1 + z]), 1.f / (kUnit<RP> * kLow), __uint_as_float(o[0][e0 + z]) * (1.f / kUnit<RP>));
                 };
                 y[i][k] = make_float2(sum_of(0), sum_of(1));
               }
@@ -765,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
       for (int j = 0; j < nb; ++j, ++g) {
         const int kb = (blk0 + j) << kLgBlk, key0 = kb + grp * KW;
         float s[KW], f[NE], vsc[NE], cand = -INFINITY;
-        uint32_t w0[KW / 4], w1[KW / 4];
+        uint32_t w0[KP / 4], w1[KP / 4], w2[RP == 128 ? KP / 4 : 1];   // of a part
         if (more) {
 #pragma unroll
           for (int u = 0; u < NE; ++u) {
@@ -846,45 +866,66 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
               }
             }
           }
-          if (half_used) {
+        }
 #pragma unroll
-            for (int c = 0; c < KW; c += 2) {
-              const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit;
+        for (int part = 0; part < PARTS; ++part) {
+          if (more && half_used) {
+#pragma unroll
+            for (int e = 0; e < KP; e += 2) {
+              const int c = part * KP + e;
+              const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit<RP>;
               const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
               l[NL > 1 ? c >> 4 : 0] += p0;
               l[NL > 1 ? c >> 4 : 0] += p1;
-              const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
-              uint16_t c0, c1;
-              uint32_t back;
-              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c0));
-              __half2 rest = __hsub2(x, *reinterpret_cast<const __half2*>(&back));
-              if (RP < 128) rest = __hmul2(rest, __float2half2_rn(kLow));
-              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
-              if ((c & 2) == 0) {
-                w0[c >> 2] = c0;
-                w1[c >> 2] = c1;
+              if constexpr (RP == 128) {
+                const __half2 x = __floats2half2_rn(p0 * vb, p1 * vb);
+                const uint32_t c0 = *reinterpret_cast<const uint32_t*>(&x) & 0xff00ff00u;
+                const __half2 rest = __hsub2(x, *reinterpret_cast<const __half2*>(&c0));
+                const uint32_t c1 = *reinterpret_cast<const uint32_t*>(&rest) & 0xff00ff00u;
+                const __half2 last = __hsub2(rest, *reinterpret_cast<const __half2*>(&c1));
+                const uint32_t c2 = *reinterpret_cast<const uint32_t*>(&last) + 0x00800080u;
+                // four keys a word: the upper bytes of two pairs
+                w0[e >> 2] = c & 2 ? __byte_perm(w0[e >> 2], c0, 0x7531) : c0;
+                w1[e >> 2] = c & 2 ? __byte_perm(w1[e >> 2], c1, 0x7531) : c1;
+                w2[e >> 2] = c & 2 ? __byte_perm(w2[e >> 2], c2, 0x7531) : c2;
               } else {
-                w0[c >> 2] |= static_cast<uint32_t>(c0) << 16;
-                w1[c >> 2] |= static_cast<uint32_t>(c1) << 16;
+                const __half2 x = __floats2half2_rn(fmaf(p0, vb, spread(c)), fmaf(p1, vb, spread(c + 1)));
+                uint16_t c0, c1;
+                uint32_t back;
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c0));
+                const __half2 rest = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLow));
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c1) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+                if ((c & 2) == 0) {
+                  w0[e >> 2] = c0;
+                  w1[e >> 2] = c1;
+                } else {
+                  w0[e >> 2] |= static_cast<uint32_t>(c0) << 16;
+                  w1[e >> 2] |= static_cast<uint32_t>(c1) << 16;
+                }
               }
             }
           }
-        }
-        if (j == 0 && item > 0) finish();
-        if (!more) break;
-        // the P buffer was last read by P V of block g - PB
-        if (g >= PB) wait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1);
-        if (mine) {
-          uint8_t* pp = pbuf + (g % PB) * C::kPTile;
+          if (part == 0) {
+            if (j == 0 && item > 0) finish();
+            // the P buffer was last read by P V of block g - PB
+            if (more && g >= PB) wait(&pv_done[(g - PB) & 1], ((g - PB) >> 1) & 1);
+          }
+          if (more && mine) {
+            uint8_t* pp = pbuf + (g % PB) * C::kPTile;
 #pragma unroll
-          for (int u = 0; u < NE; ++u) {
-            *reinterpret_cast<uint4*>(pp + swz128(p_row, NE * grp + u)) =
-                make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
-            *reinterpret_cast<uint4*>(pp + (RP == 128 ? kPBytes + swz128(p_row, NE * grp + u) : swz128(p_row + RQ, NE * grp + u))) =
-                make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
+            for (int u = 0; u < NE / PARTS; ++u) {
+              const int at = NE * grp + part * (NE / PARTS) + u;
+              *reinterpret_cast<uint4*>(pp + swz128(p_row, at)) = make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
+              *reinterpret_cast<uint4*>(pp + (RP == 128 ? kPBytes + swz128(p_row, at) : swz128(p_row + RQ, at))) =
+                  make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
+              if constexpr (RP == 128)
+                *reinterpret_cast<uint4*>(pp + 2 * kPBytes + swz128(p_row, at)) =
+                    make_uint4(w2[4 * u], w2[4 * u + 1], w2[4 * u + 2], w2[4 * u + 3]);
+            }
           }
         }
+        if (!more) break;
         // ---- value rows no row of the item may use: zero them (two threads per key)
         {
           const int key = kb + (st >> 1);

@@ -112,8 +112,8 @@ struct QAttnArgs {
   float2* part_ml;              // [B * Hkv][n_splits][rows] (reference, sum of exponentials)
   uint16_t* out;
 };
-// Query rows of an item.  128 (prompt chunks) sum both codes of the weights in one
-// accumulator, so calls whose rows' bits must not depend on n take 32 or 64.
+// Query rows of an item.  128 (prompt chunks) hold the weights in other codes, so calls
+// whose rows' bits must not depend on n take 32 or 64.
 inline int qattn_rows(int n, int64_t rows) { return rows <= 32 ? 32 : rows <= 64 || n <= SPEC_MAX_K + 1 ? 64 : 128; }
 // Keys any row of a sequence may see, as whole blocks; none: blocks = 0.
 constexpr int kQBlk = 128;   // keys of one MMA block
