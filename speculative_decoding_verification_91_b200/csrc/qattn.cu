@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
             sum[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < NG * NL; ++e) sum[i] += l_s[e * RP + r];
-            if (bad_s[r] != 0.f) sum[i] = __int_as_float(0x7fffffff);    // a NaN query
+            if (bad_s[r] != 0.f && sum[i] != 0.f) sum[i] = __int_as_float(0x7fffffff);    // a NaN query (no key: zero)
           }
         }
         // 64 columns of eight rows at a time, or 32 of 16 or (w0 and w1 summed already) 32

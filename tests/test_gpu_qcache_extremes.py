@@ -69,3 +69,28 @@ def test_a_dominant_key_leaves_the_others_their_weight(batch, n, G, D, L, block,
     # the least steps, up to 4096 keys off by less than one of 2^-18 (deviation 0.41) whose values are of size 1.4
     # against a result of 0.06 and more, 0.0023; together below 2^-7.
     assert worst <= 2.0 ** -7, worst
+
+
+@pytest.mark.parametrize("n,Hq", [(3, 2), (9, 8), (20, 8)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_row_without_a_key_is_zero_whatever_its_query_holds(n, Hq, bad):
+    """A short window past the cache leaves all rows but the first without a key.  Their results are zero, with
+    a NaN among their queries too, in a table of one split (results written at once) and in a wide one (joined)."""
+    H, D = 1, 128
+    c = Cache(200, [40], 1, H, D, 16, 128)
+    c.fill()
+    q = c.rows(n, Hq)
+    q[0, 1:, :, 7] = bad
+    q[0, 0, 1, 3] = bad                                  # this row sees key 39
+    outs = []
+    for pages in (1, 64):
+        table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+        table[:, :1] = c.d["table"][:, :1]
+        ws = torch.zeros(B.spec_qcache_attn_workspace_bytes(c.desc, Hq, 1, n, pages, 3), dtype=torch.uint8, device="cuda")
+        out = torch.full_like(q, 3.0)
+        B.spec_qcache_attn(c.desc, None, q, Hq * D, Hq, table, pages, c.d["lens"], 1, n, 1, 0, 3, 0.0, out, ws, ws.numel())
+        assert B.spec_read_device_status(ws, ws.numel()) == 0
+        outs.append(out)
+        assert torch.all(out[0, 1:] == 0)
+        assert torch.all(torch.isnan(out[0, 0, 1])) and not torch.isnan(out[0, 0, 0]).any()
+    assert torch.equal(outs[0][0, 0, 0], outs[1][0, 0, 0])
