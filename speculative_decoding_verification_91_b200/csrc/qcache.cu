@@ -61,8 +61,9 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // an SM, spill (103 and 119 us).
 //
 // Codes are those of the exactly turned key.  Keys turn in binary32, off by less
-// than kTurnErr (|x0| + |x1|) magnitude: cosine and sine 1.5 steps and a rounding by
-// the magnitude each, the product, the sum, 4.5 x 2^-24.  Where rounding that much
+// than kTurnErr (|x0| + |x1|) magnitude: cosine and sine 1.5 steps, the magnitude's own
+// rounding to binary32 and that of its product with them, the product with the entry,
+// the sum: 5.5 x 2^-24.  Where rounding that much
 // lower and higher (by a lane's largest own and partner's magnitude) gives two codes
 // (3 in 10^4) the entry is formed again in binary64, all of a CTA's together at its
 // end.  Blocks with infinities or NaN and half pairs
@@ -70,7 +71,7 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // of it in binary64, with each head its own angles, took 545 us for 64 x 256 tokens
 // of 8 heads; entries formed again where they were found, 160-230; a warp a head that
 // reads its rows twice, 135.)
-constexpr float kTurnErr = 4.6f / 16777216.f;
+constexpr float kTurnErr = 5.6f / 16777216.f;
 
 __device__ __forceinline__ __nv_bfloat162 abs2(uint32_t w) {
   w &= 0x7fff7fffu;
@@ -238,7 +239,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
     };
     const bool exact = m >= 0x7f800000u;     // (uniform in the CTA)
     // the scale turns at 1.75 x 2^x: a turned magnitude is within 2 kTurnErr of the
-    // largest, 8 steps of binary32, of itself.  Next to that the largest is found in
+    // largest, 10 steps of binary32, of itself.  Next to that the largest is found in
     // binary64, among the entries that may be above (every block with one in a hundred
     // amaxes of bf16 comes here; all entries in binary64 took 40 us)
     if (turns_keys && !exact && abs(static_cast<int>(m & 0x7fffffu) - 0x600000) <= 16) {

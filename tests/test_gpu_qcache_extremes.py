@@ -8,7 +8,7 @@ import torch
 from oracle import qcache as Q
 from speculative_decoding_verification_91_b200 import binding as B
 
-from .test_gpu_qcache import HALF_BF16, Cache, attend
+from .test_gpu_qcache import HALF_BF16, Cache, attend, rope_config, turned, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +94,37 @@ def test_a_row_without_a_key_is_zero_whatever_its_query_holds(n, Hq, bad):
         assert torch.all(out[0, 1:] == 0)
         assert torch.all(torch.isnan(out[0, 0, 1])) and not torch.isnan(out[0, 0, 0]).any()
     assert torch.equal(outs[0][0, 0, 0], outs[1][0, 0, 0])
+
+
+# ------------------------------------------------------------------------ append
+
+def append_both(c, cfg_args, k, v, cfg):
+    """The definition's append and the library's; every byte the same."""
+    freq, layout, span, magnitude = cfg_args
+    B_, n = k.shape[:2]
+    for b, L in enumerate(c.lens):
+        Q.append(c.k, c.ks, c.block, c.table[b], L, turned(k[b], L, freq, layout, span, magnitude))
+        Q.append(c.v, c.vs, c.block, c.table[b], L, v[b].double().cpu().numpy())
+    ws = workspace(B.spec_qcache_write_workspace_bytes(c.desc, B_, n))
+    B.spec_qcache_write(c.desc, cfg, c.d["table"], c.max_pages, c.d["lens"], B_, n, k, c.H * c.D, v, c.H * c.D, ws,
+                        ws.numel())
+    assert B.spec_read_device_status(ws, ws.numel()) == 0
+    c.same()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("magnitude", [1.2772588722239782, 1.0 + 1.98 * 2.0 ** -25, 1.0 - 0.98 * 2.0 ** -25, 0.1])
+def test_write_with_a_magnitude_that_binary32_does_not_hold(layout, magnitude):
+    """Ordinary keys, and keys next to a rounding border and to where the scale turns, with angles of nearly 0:
+    the binary64 magnitude decides the side."""
+    H, D, n, block = 2, 256, 70, 64
+    c = Cache(7, [64, 3], n, H, D, block)
+    c.fill()
+    shape = (2, n, H, D)
+    border = (1 + (2 * c.rng.integers(0, 8, shape) + 1) / 16) * 2.0 ** c.rng.integers(-2, 3, shape)
+    border[:, 0] = 7.0 / 4
+    x = np.where(c.rng.random(shape) < 0.1, border, c.rng.normal(size=shape)).clip(-1.75, 1.75)
+    for kw in (dict(scaling="linear", factor=1e12), dict(scaling="parts", factor=16.0, original=8192.0)):
+        k, v = torch.from_numpy(x).to(torch.bfloat16).cuda(), c.rows(n, H)
+        append_both(c, (Q.rope_frequencies(256, 128, 10000.0, **kw), layout, 256, magnitude), k, v,
+                    rope_config(256, 128, layout, magnitude=magnitude, **kw))

@@ -39,3 +39,18 @@ def test_shared_memory_read_in_16_byte_pieces_is_aligned_to_them():
             only_small = not re.search(r"float4\*>\([^;]*\b%s\b" % var, text) and kind in ("float2", "unsigned long long")
             assert align or by_hand or kind == "uint4" or only_small, (name, var)
     assert seen >= 5
+
+
+def test_the_error_bound_of_turned_keys_counts_every_rounding():
+    """In units of 2^-24 (|x0| + |x1|) magnitude.  Cosine and sine: 1 of the function (one step below 1), half of
+    the sum with the angle's tail.  The magnitude: 1/2 step, 1, of its conversion to binary32 (of itself at most
+    2^-24), 1 of its product with each.  The entry: 1 of the product that is rounded, 1 of the sum."""
+    need = 1.0 + 0.5 + 1.0 + 1.0 + 1.0 + 1.0
+    text = source("qcache.cu")
+    have = float(re.search(r"kTurnErr = ([\d.]+)f / 16777216\.f;", text).group(1))
+    assert have > need
+    # the largest entry may be off by twice that bound of itself (its pair's partner is no larger), in steps of
+    # binary32 at 1.75 x 2^x: all of those next to the scale's turn are formed again
+    steps = 2 * have * 2.0 ** -24 * 1.75 / 2.0 ** -23
+    near, least = re.search(r"- 0x600000\) <= (\d+)\)", text), re.search(r"\| 0x600000u\) - (\d+);", text)
+    assert steps < int(near.group(1)) and steps < int(least.group(1))
