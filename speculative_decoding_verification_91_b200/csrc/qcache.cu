@@ -27,9 +27,9 @@ __device__ __forceinline__ float to_odd(double y) {
   return static_cast<double>(f) == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// Element d of a head of the row at p, turned by r at pos, rounded to odd.
+// Element d of a head of the row at p, turned by r at pos.
 // (Out of line: needed for a few entries in 10^4.)
-__device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d, int pos) {
+__device__ __noinline__ double turned(const RopeArgs& r, const uint16_t* p, int d, int pos) {
   const int half = r.span / 2;
   int j = -1, e = d;          // pair and partner dim
   bool second = false;
@@ -40,13 +40,13 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
     j = d >> 1, e = d ^ 1, second = d & 1;
   }
   const double x = bf16_to_f32(p[d]);
-  if (j < 0) return static_cast<float>(x);
+  if (j < 0) return x;
   const double w = bf16_to_f32(p[e]);
   double c, s;
   rope_turn(pos, r.step[j], c, s);
   c *= r.magnitude;
   s *= r.magnitude;
-  return to_odd(second ? w * s + x * c : x * c - w * s);
+  return second ? w * s + x * c : x * c - w * s;
 }
 
 // The append.  A CTA takes one touched block of BT tokens of a sequence, keys (the
@@ -66,8 +66,8 @@ __device__ __noinline__ float turned(const RopeArgs& r, const uint16_t* p, int d
 // the sum: 5.5 x 2^-24.  Where rounding that much
 // lower and higher (by a lane's largest own and partner's magnitude) gives two codes
 // (3 in 10^4) the entry is formed again in binary64, all of a CTA's together at its
-// end.  Blocks with infinities or NaN and half pairs
-// whose distance is no multiple of 8 take binary64 throughout.  (All
+// end.  Blocks with infinities or NaN, those that keep a scale that is no power of two
+// and half pairs whose distance is no multiple of 8 take binary64 throughout.  (All
 // of it in binary64, with each head its own angles, took 545 us for 64 x 256 tokens
 // of 8 heads; entries formed again where they were found, 160-230; a warp a head that
 // reads its rows twice, 135.)
@@ -234,7 +234,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
         const int t = t0 + i * RI;
 #pragma unroll 1
         for (int e = 0; e < 8; ++e)
-          f(t, e, is_v ? bf16_to_f32(head0[t * stride + d0 + e]) : turned(r, head0 + t * stride, d0 + e, p0 + t));
+          f(t, e, is_v ? static_cast<double>(bf16_to_f32(head0[t * stride + d0 + e])) : turned(r, head0 + t * stride, d0 + e, p0 + t));
       }
     };
     const bool exact = m >= 0x7f800000u;     // (uniform in the CTA)
@@ -253,7 +253,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
       float top = 0.f;
       for (; may; may &= may - 1) {
         const int k = __ffsll(static_cast<long long>(may)) - 1, t = t0 + k / 8 * RI;
-        top = fmaxf(top, fabsf(turned(r, head0 + t * stride, d0 + k % 8, p0 + t)));
+        top = fmaxf(top, fabsf(to_odd(turned(r, head0 + t * stride, d0 + k % 8, p0 + t))));
       }
       __syncthreads();
       m = block_max(top, h & 1);
@@ -261,7 +261,8 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
     if (exact) {
       bool bad = false;
       amax = 0.f;
-      entries([&](int, int, float v) {
+      entries([&](int, int, double y) {
+        const float v = to_odd(y);
         if (finite_f(v)) amax = fmaxf(amax, fabsf(v));
         else bad = true;
       });
@@ -275,22 +276,29 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
     uint8_t* dst = (is_v ? c.v : c.k) + (head * kPg + p0 % kPg) * D;
     const int e2 = scale_exponent(amax);
     float now = pow2f(e2), inv = pow2f(-e2);
+    bool divide = false;                       // a scale that is no power of two: nothing of it is exact in binary32
     if (lo > 0) {                              // committed tokens share the block
       const float was = *sc;
+      const bool odd = __float_as_uint(was) & 0x7fffffu;
       now = fmaxf(now, was);
-      if (now == was) inv = __fdiv_rn(1.f, was);
+      divide = odd && now == was;
+      if (now == was && !odd) inv = __fdiv_rn(1.f, was);
       if (now > was) {                         // rewrite their codes for the larger scale
         const float ratio = __fdiv_rn(was, now);
+        auto scaled = [&](float v) {           // (a code times the ratio: 28 bits where the ratio has 24)
+          return v != v ? 0.f : odd ? to_odd(static_cast<double>(v) * ratio) : v * ratio;
+        };
         for (int i = threadIdx.x; i < lo * D / 2; i += kWriteThreads) {
           uint16_t* q = reinterpret_cast<uint16_t*>(dst) + i;
           const float2 v = e4m3_values(*q);
-          *q = e4m3x2(v.x == v.x ? v.x * ratio : 0.f, v.y == v.y ? v.y * ratio : 0.f);
+          *q = e4m3x2(scaled(v.x), scaled(v.y));
         }
       }
     }
-    if (exact) {
-      entries([&](int t, int e, float v) {
-        dst[t * D + d0 + e] = static_cast<uint8_t>(e4m3x2(v == v ? v * inv : 0.f, 0.f));
+    if (exact || divide) {
+      entries([&](int t, int e, double y) {
+        const float v = to_odd(divide ? y / now : y * inv);
+        dst[t * D + d0 + e] = static_cast<uint8_t>(e4m3x2(v == v ? v : 0.f, 0.f));
       });
     } else {
       err *= inv;                              // (0 where nothing turns, and for rows of zeros)
@@ -329,9 +337,9 @@ __device__ __forceinline__ void write_block(const RopeArgs& r, const QWriteArgs&
     const int h = h0 + (all ? i / D / (hi - lo) : static_cast<uint32_t>(s.list[i].x) >> 16);
     const int t = all ? lo + i / D % (hi - lo) : s.list[i].x >> 8 & 0xff, d = all ? i % D : s.list[i].x & 0xff;
     const int64_t head = static_cast<int64_t>(page) * c.n_kv_heads + h;
-    const float inv = all ? __fdiv_rn(1.f, c.ks[head * (kPg / BT) + (p0 % kPg) / BT]) : __int_as_float(s.list[i].y);
-    const float v = turned(r, block0 + t * stride + h * D, d, p0 + t);
-    c.k[(head * kPg + p0 % kPg + t) * D + d] = static_cast<uint8_t>(e4m3x2(v == v ? v * inv : 0.f, 0.f));
+    const double y = turned(r, block0 + t * stride + h * D, d, p0 + t);
+    const float v = to_odd(all ? y / c.ks[head * (kPg / BT) + (p0 % kPg) / BT] : y * __int_as_float(s.list[i].y));
+    c.k[(head * kPg + p0 % kPg + t) * D + d] = static_cast<uint8_t>(e4m3x2(v == v ? v : 0.f, 0.f));
   }
 }
 

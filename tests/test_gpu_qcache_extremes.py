@@ -128,3 +128,41 @@ def test_write_with_a_magnitude_that_binary32_does_not_hold(layout, magnitude):
         k, v = torch.from_numpy(x).to(torch.bfloat16).cuda(), c.rows(n, H)
         append_both(c, (Q.rope_frequencies(256, 128, 10000.0, **kw), layout, 256, magnitude), k, v,
                     rope_config(256, 128, layout, magnitude=magnitude, **kw))
+
+
+@pytest.mark.parametrize("D,block", [(128, 16), (256, 64)])
+@pytest.mark.parametrize("turn", ["as given", "half", "interleaved"])
+def test_write_beside_committed_tokens_of_any_scale(D, block, turn):
+    """Pools filled by other means: scales that are no powers of two, chosen so that an entry lies within
+    2^-24 of a rounding border of theirs; then new rows that raise them, with a committed code next to a border."""
+    H, n, Bn = 4, 5, 24
+    rng = np.random.default_rng(D)
+    lens = rng.integers(1, block - n, Bn) + block * rng.integers(0, 4, Bn)
+    c = Cache(8, [int(x) for x in lens], n, H, D, block)
+    c.fill(0.3)
+    k, v = c.rows(n, H), c.rows(n, H)
+    for b, L in enumerate(lens):
+        page, at = c.table[b, L // 64], (L % 64) // block
+        first = L % 64 // block * block
+        for s, x, pool in ((c.ks, k, c.k), (c.vs, v, c.v)):
+            for h in range(H):
+                border = (1 + (2 * rng.integers(0, 8) + 1) / 16) * 2.0 ** rng.integers(0, 4)
+                if b % 2 == 0:
+                    # the scale stays: a new entry / scale next to the border
+                    x0 = 1 + rng.integers(0, 128) / 128
+                    s[page, h, at] = np.float32(x0 / border)
+                    x[b, rng.integers(0, n), h, D - 1 - rng.integers(0, 30)] = x0
+                else:
+                    # it rises to 1: a committed code x scale next to the border
+                    m = int(rng.integers(0, 8))
+                    s[page, h, at] = np.float32(border / 16 / (1 + m / 8))
+                    pool[page, h, first:first + 1, ::3] = 7 << 3 | m
+                    x[b, 0, h, D - 1] = 448.0
+    c.upload()
+    # angles of nearly 0; "half" with an odd distance takes binary64 throughout
+    kw = dict(scaling="linear", factor=1e12)
+    span = {"as given": D, "half": D - 2, "interleaved": D}[turn]
+    n_rot = 0 if turn == "as given" else 40
+    layout = "interleaved" if turn == "interleaved" else "half"
+    append_both(c, (Q.rope_frequencies(span, n_rot, 10000.0, **kw), layout, span, 1.0), k, v,
+                None if turn == "as given" else rope_config(span, n_rot, layout, **kw))
