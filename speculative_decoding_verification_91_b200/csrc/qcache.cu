@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(kWriteThreads, 2) qcache_write_kernel(const __
 // first code keeps 4 significant bits, the second 4 of what is left, so the two
 // hold a query to 2^-9 of itself (and 2^-19 of the row's largest), finer than
 // bf16's 2^-9 on average, and both factors of the score product are e4m3.  A
-// row with an infinity or NaN gets a NaN scale, which makes its result NaN.
+// row with an infinity, a NaN or a magnitude beyond the largest scale's codes gets a
+// NaN scale, which makes its result NaN.
 // A CTA takes a row of a sequence and every blockIdx.y-th four of its heads, a warp a head (4 or
 // 8 dims a lane, one load): the row's angles once for all of them (each warp forming its own
 // took 41 us for 512 rows of 32 heads, 12.5 now), the first head asked for before.  Few rows: 4.5
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(128) qcache_query_kernel(const __grid_constant
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    bad = __any_sync(0xffffffffu, bad);
+    bad = __any_sync(0xffffffffu, bad) || amax > 448.f * 0x1p100f;   // (codes would saturate)
     const int e2 = scale_exponent(amax);
     const float inv = pow2f(-e2);
     const int h = hq / a.G, g = hq % a.G;

@@ -8,7 +8,7 @@ import torch
 from oracle import qcache as Q
 from speculative_decoding_verification_91_b200 import binding as B
 
-from .test_gpu_qcache import HALF_BF16, Cache, attend, rope_config, turned, workspace
+from .test_gpu_qcache import HALF_BF16, Cache, attend, check_attention, rope_config, turned, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,27 @@ def test_write_beside_committed_tokens_of_any_scale(D, block, turn):
     layout = "interleaved" if turn == "interleaved" else "half"
     append_both(c, (Q.rope_frequencies(span, n_rot, 10000.0, **kw), layout, span, 1.0), k, v,
                 None if turn == "as given" else rope_config(span, n_rot, layout, **kw))
+
+
+# -------------------------------------------------------- queries and scores out of the ordinary
+
+@pytest.mark.parametrize("n,Hq", [(2, 2), (17, 4), (20, 8)])
+def test_queries_too_large_for_their_codes_are_nan(n, Hq):
+    """Codes reach 448 x 2^100 = 5.68e32, as a query stands or as it is turned.  A row beyond is NaN, and no
+    other; one just below gives its result (keys of 2^-100)."""
+    H, D, L = 2, 128, 150
+    c = Cache(300, [L], 1, H, D, 32, 128)
+    k, v = c.rng.normal(size=(L, H, D)) * 2.0 ** -100, c.rng.normal(size=(L, H, D))
+    for rows, pool, s in ((k, c.k, c.ks), (v, c.v, c.vs)):
+        Q.append(pool, s, 32, c.table[0], 0, rows)
+    c.upload()
+    q = c.rows(n, Hq, 2.0 ** 98)
+    q[0, 0, 0, 5], q[0, 1, 1, 77] = 5.7e32, -5.6e32
+    plain = attend(c, None, q, Hq, n, extra=0)
+    assert torch.all(torch.isnan(plain[0, 0, 0])) and torch.isnan(plain).sum() == D
+    q[0, 0, 0, 5] = 3.0e32
+    turned_q = attend(c, rope_config(D, 0, magnitude=1.5), q, Hq, n, extra=0)   # nothing turns, nothing is scaled
+    assert not torch.isnan(turned_q).any()
+    more = attend(c, rope_config(D, D // 2, magnitude=4.0), q, Hq, n, extra=0)
+    assert torch.all(torch.isnan(more[0, 0, 0])) and torch.all(torch.isnan(more[0, 1, 1])) and torch.isnan(more).sum() == 2 * D
+    check_attention(c, q, turned_q, (Q.rope_frequencies(D, 0), "half", D, 1.0), 0, 0, 0)
