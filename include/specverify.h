@@ -486,7 +486,8 @@ size_t spec_qcache_attn_workspace_bytes(const spec_qcache* c, int n_q_heads, int
  *   out [B][n][n_q_heads][head_dim] bf16; scale 0 = 1/sqrt(head_dim).
  * n in [1, SPEC_MAX_PREFILL], q_offset and kv_extra in [0, 65536].  A query row
  * with an infinity, a NaN or, as turned, a magnitude above 448 * 2^100 gives a row
- * of NaN (zeros where it sees no key) and touches no other.  Keys on a
+ * of NaN (zeros where it sees no key) and touches no other.  So does a row whose
+ * largest score, as keys are read, passes 2.9e6 (2^22 in powers of two) from zero.  Keys on a
  * page id outside the pool are left out (SPEC_DEV_BAD_PAGE); a sequence whose
  * length is negative or whose keys do not fit its block-table row gives zeros
  * (SPEC_DEV_BAD_LENGTH).

@@ -94,7 +94,11 @@ constexpr float kLazy = 3.5f;
 template <int RP>
 constexpr float kUnit = RP == 128 ? 2048.f : 32.f;
 constexpr float kLow = 16.f;               // w1 is stored times 16
-constexpr float kNoKey = -1e30f;           // reference of a row that has seen no key
+constexpr float kNoKey = -0x1.fffffep127f;   // reference of a row that has seen no key
+// References further than this from 0 are off by 1/4 and more, and with them 2^(s - m);
+// a row that comes to one ends as NaN.
+constexpr float kFar = 0x1p22f;
+constexpr float kMostFactor = 4e30f;       // of a score's e4m3 products (below 2^26): the score stays finite
 
 // Waits for this thread's loads from TMEM, v's among them.
 template <int N>
@@ -791,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
           for (int u = 0; u < NE; ++u) {
             const int e = ((j << kLgBlk) + grp * KW + 16 * u) >> lg_bt;
             vsc[u] = vs[e];
-            f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), 3e38f);
+            f[u] = fminf(fmaxf(qs * ks[e], 1e-30f), kMostFactor);
           }
           wait(&s_full[g % SB], (g / SB) & 1);
           __syncwarp();
@@ -840,6 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
               mref = bm;
 #pragma unroll
               for (int u = 0; u < NL; ++u) l[u] *= al;
+              if (fabsf(bm) > kFar) l[0] = __int_as_float(0x7fffffff);
             }
             if (j > 0) {
               // the running sums of the rows that moved (all earlier P V done)

@@ -190,3 +190,67 @@ def test_queries_too_large_for_their_codes_are_nan(n, Hq):
     more = attend(c, rope_config(D, D // 2, magnitude=4.0), q, Hq, n, extra=0)
     assert torch.all(torch.isnan(more[0, 0, 0])) and torch.all(torch.isnan(more[0, 1, 1])) and torch.isnan(more).sum() == 2 * D
     check_attention(c, q, turned_q, (Q.rope_frequencies(D, 0), "half", D, 1.0), 0, 0, 0)
+
+
+@pytest.mark.parametrize("n,Hq,window", [(1, 2, 0), (5, 16, 0), (20, 16, 300), (2, 4, 60)])
+@pytest.mark.parametrize("size", [1e3, 2.0 ** 17, 2.0 ** 21, 2.0 ** 25, 1e20, 1e31, 1e36])
+def test_scores_of_any_size(n, Hq, window, size):
+    """Scores that pick one key, above and below zero, values of scales of their own; all keys alike at such
+    scores: their mean.  Past 2.9e6 binary32 leaves no room for differences: NaN, not something else."""
+    H, D, L, block = 1, 128, 700, 16
+    c = Cache(400, [L], 1, H, D, block, 128)
+    k, v = np.zeros((L, H, D)), c.rng.normal(size=(L, H, D))
+    v *= 2.0 ** c.rng.integers(-6, 7, (L, 1, 1))
+    steps = c.rng.permutation(L)
+    k[:, 0, 0], k[:, 0, 1], k[:, 0, 2] = steps // 14, steps % 14, 1.0
+    for rows, pool, s in ((k, c.k, c.ks), (v, c.v, c.vs)):
+        Q.append(pool, s, block, c.table[0], 0, rows)
+    c.upload()
+    q = torch.zeros(1, n, Hq, D, dtype=torch.bfloat16, device="cuda")
+    ws = workspace(B.spec_qcache_attn_workspace_bytes(c.desc, Hq, 1, n, c.max_pages, window))
+    sign = torch.tensor([1.0, -1.0], device="cuda").repeat(Hq // 2)
+    scale = float(np.float32(size / 700))
+
+    def run():
+        out = torch.empty_like(q)
+        B.spec_qcache_attn(c.desc, None, q, Hq * D, Hq, c.d["table"], c.max_pages, c.d["lens"], 1, n, 0, 0, window, scale,
+                           out, ws, ws.numel())
+        assert B.spec_read_device_status(ws, ws.numel()) == 0
+        return out.double().cpu().numpy()
+
+    slot, pages = np.arange(L) % 64, c.table[0][np.arange(L) // 64]
+    V = Q.VALUES[c.v[pages, 0, slot]] * c.vs[pages, 0, slot // block, None].astype(float)
+    K = Q.VALUES[c.k[pages, 0, slot]][:, :3] * c.ks[pages, 0, slot // block, None].astype(float)
+    limit = 2.0 ** 22 / math.log2(math.e)
+    picked = 0
+    for offset in (0.0, -1024.0):
+        q[..., 0], q[..., 1], q[..., 2] = 16 * sign, sign, offset
+        out = run()
+        for i in range(n):
+            seen = np.arange(L) > L + i - window if window else np.ones(L, dtype=bool)
+            for h in range(Hq):
+                s = np.where(seen, K @ q[0, i, h, :3].double().cpu().numpy(), -np.inf)
+                top, j = np.sort(s)[-2:], int(np.argmax(s))
+                if abs(top[1]) * scale > limit * 1.001:
+                    assert np.all(np.isnan(out[0, i, h])), (offset, i, h)
+                    continue
+                if (top[1] - top[0]) * scale < 100:      # the keys' codes may make two alike
+                    continue
+                if np.abs(s[seen]).max() * scale > limit * 0.999 and np.all(np.isnan(out[0, i, h])):
+                    continue                             # keys beyond the limit came first
+                picked += 1
+                # one weight, coded: the steps above, and the result's own rounding
+                bound = (HALF_BF16 + SHARE) * 1.01 * np.abs(V[j])
+                assert np.all(np.abs(out[0, i, h] - V[j]) <= bound), (offset, i, h)
+    assert picked or size > limit or size < 2.0 ** 17    # (scores 100 apart there are none at 1e3)
+    q[..., 0], q[..., 1], q[..., 2] = 0.0, 0.0, 700 * sign
+    out = run()
+    if size > limit:
+        assert np.all(np.isnan(out))
+        return
+    for i in range(n):
+        seen = np.arange(L) > L + i - window if window else np.ones(L, dtype=bool)
+        mean, mass = V[seen].mean(0), np.abs(V[seen]).mean(0)
+        tail = np.abs(V[seen]).max()                     # the least steps, up to each key's values' largest
+        bound = HALF_BF16 * np.abs(mean) + (SHARE + 2.0 ** -16) * mass + LEAST_FEW * tail
+        assert np.all(np.abs(out[0, i] - mean) <= bound), (i, "mean")
