@@ -168,7 +168,8 @@ bool attn_layout(const spec_qcache* c, int n_q_heads, int B, int n, int max_page
 }
 
 // Bytes for any call up to these sizes.  A call of fewer sequences or rows may
-// take a shorter split: with n <= SPEC_MAX_K + 1 the cache's own, beyond that one
+// take a shorter split: with n <= SPEC_MAX_K + 1 the cache's own (of which it may have
+// kMaxQSplits, so a chunk's table may be wider than such a call's), beyond that one
 // that leaves at most kItemsWanted + (row blocks) items of 64 rows.
 size_t attn_bytes(const spec_qcache* c, int n_q_heads, int B, int n, int max_pages, int window) {
   AttnLayout s;
@@ -176,7 +177,8 @@ size_t attn_bytes(const spec_qcache* c, int n_q_heads, int B, int n, int max_pag
   size_t total = s.total;
   if (n > SPEC_MAX_K + 1) {
     AttnLayout v;
-    if (!attn_layout(c, n_q_heads, B, SPEC_MAX_K + 1, max_pages, window, &v)) return 0;
+    const int64_t widest = (int64_t)kMaxQSplits * split_of(c) / SPEC_PAGE_SIZE;
+    if (!attn_layout(c, n_q_heads, B, SPEC_MAX_K + 1, (int)(max_pages < widest ? max_pages : widest), window, &v)) return 0;
     const uint64_t rows = (uint64_t)B * n * n_q_heads, blocks = rows / 64 + (uint64_t)B * c->n_kv_heads;
     const uint64_t cap = ((uint64_t)max_pages * SPEC_PAGE_SIZE + 4095) / 4096;
     const uint64_t slots = 128 * (kItemsWanted + 2 * blocks) + rows * (cap + 1);
