@@ -383,11 +383,11 @@ typedef struct spec_rope_config {
   int n_rot;           /* turned pairs, 0..span/2 */
   int scaling;         /* SPEC_ROPE_PLAIN .. SPEC_ROPE_PARTS */
   double theta;        /* base, > 0 */
-  double factor;       /* S >= 1 (PLAIN: ignored) */
+  double factor;       /* S >= 1 (PLAIN: ignored; RAISED: the raised base is finite) */
   double original;     /* PARTS: the original length, > 0 */
   double turns_lo;     /* PARTS: 0 <= turns_lo < turns_hi */
   double turns_hi;
-  double magnitude;    /* > 0, multiplies cos and sin */
+  double magnitude;    /* multiplies cos and sin: a normal binary32 number > 0 */
 } spec_rope_config;
 
 /* Host: the n_rot frequencies f_j (binary64).  out: host array, n_rot long. */

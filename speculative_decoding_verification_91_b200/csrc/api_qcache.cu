@@ -1,6 +1,7 @@
 // C ABI of the rotary operator and the 8-bit cache: argument checks, workspace
 // layout, launches.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -33,7 +34,8 @@ int rope_frequencies(const spec_rope_config* r, int head_dim, double* f) {
   if (r->span < 2 || r->span % 2 || r->span > head_dim || r->n_rot < 0 || r->n_rot > r->span / 2)
     return SPEC_EINVAL;
   if (r->scaling < SPEC_ROPE_PLAIN || r->scaling > SPEC_ROPE_PARTS) return SPEC_EINVAL;
-  if (!(r->theta > 0.0) || !isfinite(r->theta) || !(r->magnitude > 0.0) || !isfinite(r->magnitude))
+  // (the kernels take the magnitude in binary32)
+  if (!(r->theta > 0.0) || !isfinite(r->theta) || !(r->magnitude >= FLT_MIN) || r->magnitude > FLT_MAX)
     return SPEC_EINVAL;
   if (r->scaling != SPEC_ROPE_PLAIN && (!(r->factor >= 1.0) || !isfinite(r->factor))) return SPEC_EINVAL;
   if (r->scaling == SPEC_ROPE_RAISED && r->span < 4) return SPEC_EINVAL;
@@ -43,6 +45,7 @@ int rope_frequencies(const spec_rope_config* r, int head_dim, double* f) {
     return SPEC_EINVAL;
   double base = r->theta;
   if (r->scaling == SPEC_ROPE_RAISED) base *= pow(r->factor, (double)r->span / (r->span - 2));
+  if (!isfinite(base)) return SPEC_EINVAL;
   // base^(-2j / span) as a product of two powers (16 + 8 of them instead of 128, of
   // 50 ns each, in every call): off by 3 x 2^-53 at most
   double fine[8], coarse = 1.0;
