@@ -413,7 +413,8 @@ int spec_rope(const spec_rope_config* r, int dtype, const void* x, int64_t x_row
  * codes (1 sign, 4 exponent, 3 fraction bits, largest 448, no infinities) with
  * one binary32 scale per (block of block_tokens tokens of a page, KV head), one
  * for keys and one for values: the entry stands for code * scale.  Half the
- * bytes of the bf16 pools, of which the verify step reads every one.
+ * bytes of bf16 pools with values of their own; a key-equals-value layer's bf16
+ * pools hold 2.5 bytes per key dim (a quarter of the pairs turned), these 2.
  *
  * spec_qcache_write chooses powers of two: the least 2^e with
  * amax <= 448 * 2^e, e in [-100, 100] (2^-100 for a block of zeros; magnitudes
@@ -427,7 +428,8 @@ int spec_rope(const spec_rope_config* r, int dtype, const void* x, int64_t x_row
  * enter the scale, an infinity is stored as the largest code, NaN as 0: pages
  * hold finite numbers only, so a masked entry cannot reach a result.
  * Pools filled by other means may carry any finite scale in [2^-100, 2^100]
- * (zero too, for a block of zeros).
+ * (zero too, for a block of zeros); the codes of tokens that a call reads must be
+ * numbers: one NaN code among them makes rows NaN that do not see it.
  *
  * Layouts, 16-byte aligned:
  *   k_pool, v_pool   [num_pages][n_kv_heads][page_size][head_dim] e4m3
@@ -440,8 +442,10 @@ typedef struct spec_qcache {
   int num_pages;
   int page_size;         /* SPEC_PAGE_SIZE */
   int block_tokens;      /* tokens a scale covers: 16, 32 or 64 */
-  int split_tokens;      /* split-KV chunk of the attention: a multiple of 128 up to 4096, 0 = 1024;
-                            results depend on it, not on the batch or the rows of a call */
+  int split_tokens;      /* split-KV chunk of the attention: a multiple of 128 up to 4096, 0 = 1024.
+                            A row's bits depend on it; for n <= SPEC_MAX_K + 1 not on the batch,
+                            the rows or the block table's width of a call.  Longer calls take
+                            splits of their own, by B, n, the heads and max_pages. */
   void* k_pool;
   void* v_pool;
   void* k_scale;
@@ -491,7 +495,13 @@ size_t spec_qcache_attn_workspace_bytes(const spec_qcache* c, int n_q_heads, int
  * page id outside the pool are left out (SPEC_DEV_BAD_PAGE); a sequence whose
  * length is negative or whose keys do not fit its block-table row gives zeros
  * (SPEC_DEV_BAD_LENGTH).
- * For n <= SPEC_MAX_K + 1 a row's result does not depend on n, B or its place. */
+ * For n <= SPEC_MAX_K + 1 a row's result does not depend on n, B or its place.
+ * Precision beside the pools' own: a query is held to 2^-9 of itself and 2^-19 of its
+ * row's largest; a weight to 2^-8 of itself, and below 2^-18 of its split's largest
+ * by a spread over its neighbours whose sum holds (n > SPEC_MAX_K + 1 with more than 64
+ * rows a KV head: to 2^-27); scores, sums and the join are binary32.
+ * out may be q itself where q's rows are dense; else the two must not overlap.  A
+ * workspace serves one call at a time: calls on other streams take one of their own. */
 int spec_qcache_attn(const spec_qcache* c, const spec_rope_config* r, const void* q,
                      int64_t q_row_stride, int n_q_heads, const int32_t* block_table, int max_pages,
                      const int32_t* seq_lens, int B, int n, int q_offset, int kv_extra, int window,

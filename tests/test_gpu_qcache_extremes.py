@@ -254,3 +254,21 @@ def test_scores_of_any_size(n, Hq, window, size):
         tail = np.abs(V[seen]).max()                     # the least steps, up to each key's values' largest
         bound = HALF_BF16 * np.abs(mean) + (SHARE + 2.0 ** -16) * mass + LEAST_FEW * tail
         assert np.all(np.abs(out[0, i] - mean) <= bound), (i, "mean")
+
+
+@pytest.mark.parametrize("n,pages", [(1, 1), (5, 64), (20, 64)])
+def test_results_over_the_queries_themselves(n, pages):
+    """out = q, dense rows: the queries are read before any result is written, rows without a key included."""
+    H, Hq, D = 2, 8, 128
+    c = Cache(500, [40, 0, 33], 1, H, D, 16, 128)
+    c.fill()
+    q = c.rows(n, Hq)
+    table = torch.full((3, pages), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.max_pages] = c.d["table"][:, :pages]
+    ws = workspace(B.spec_qcache_attn_workspace_bytes(c.desc, Hq, 3, n, pages, 12))
+    outs = []
+    for out in (torch.empty_like(q), q):
+        B.spec_qcache_attn(c.desc, rope_config(D, 64), q, Hq * D, Hq, table, pages, c.d["lens"], 3, n, 9, 0, 12, 0.0, out,
+                           ws, ws.numel())
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and not outs[0][1].any() and outs[0][0, 0].any()
