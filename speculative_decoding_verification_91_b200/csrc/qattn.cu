@@ -36,10 +36,10 @@
 // Per block of 128 keys (D = 256), in SM clocks: the scores' MMAs 1024, P V 512 (1536
 // with RP = 128), a softmax warp 1650 with RP = 32, 2350 with 64 (exponentials and
 // codes 930, the largest score 250, the store of P 270, the rest latency between
-// them) and 5800 with 128, DRAM 2840 with every SM at work.  So long items of few rows
-// run at the pace of DRAM (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 425 us, 5.4
-// TB/s, the clock down to 1.45 GHz at the power limit), prompt chunks at that of the
-// softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 212 us),
+// them) and 6100 with 128, DRAM 2840 with every SM at work.  So long items of few rows
+// run at the pace of DRAM (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 432 to 465 us
+// on one GPU or another, 4.9 to 5.3 TB/s, the clock down to 1.45 GHz at the power limit), prompt
+// chunks at that of the softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 214 us),
 // and calls of some items a CTA also pay for the unequal shares of whole splits.  Not
 // kept: 16 softmax warps, a vote after the exponentials instead of before (3%
 // slower), a larger kLazy (1 to 4% faster, coarser small weights).

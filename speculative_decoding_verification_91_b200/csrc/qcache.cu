@@ -54,7 +54,7 @@ __device__ __noinline__ double turned(const RopeArgs& r, const uint16_t* p, int 
 // hold the block's new rows in registers (a lane 8 dims, IT rows of each warp), find
 // the largest magnitude, settle the scale and store the codes, the next head's rows
 // on their way meanwhile; every row is read once.  The angles of the block's rows are
-// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 67.5 us, 3.0
+// formed once, in shared memory.  64 x 256 tokens of 8 heads (201 MB): 68.8 us, 2.9
 // TB/s, bound by instruction issue with 16 warps an SM, which the rows in registers
 // allow: the second set of codes costs 10 us of it, the angles 8.  One body for keys
 // and values 74.8, one for both layouts of keys 70.6; 512 threads a CTA, or three CTAs
@@ -65,7 +65,7 @@ __device__ __noinline__ double turned(const RopeArgs& r, const uint16_t* p, int 
 // rounding to binary32 and that of its product with them, the product with the entry,
 // the sum: 5.5 x 2^-24.  Where rounding that much
 // lower and higher (by a lane's largest own and partner's magnitude) gives two codes
-// (3 in 10^4) the entry is formed again in binary64, all of a CTA's together at its
+// (4 in 10^4) the entry is formed again in binary64, all of a CTA's together at its
 // end.  Blocks with infinities or NaN, those that keep a scale that is no power of two
 // and half pairs whose distance is no multiple of 8 take binary64 throughout.  (All
 // of it in binary64, with each head its own angles, took 545 us for 64 x 256 tokens
