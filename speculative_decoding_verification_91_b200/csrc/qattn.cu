@@ -119,15 +119,18 @@ __device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&v)[32])
   tmem_ld16x256(taddr, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
   tmem_ld16x256(taddr + 32, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
 }
-// Added to the weight of key c of a block before it is coded (RP <= 64): 16 values spread evenly over one least
-// step of w1 around 0, so that weights below that step are dropped or raised to it in shares that sum to what
-// they are.  Rounded to nearest, thousands of small weights beside a dominant one (an attention sink) all went
-// the same way, while the sum of p below the line kept them: results were off by 2 to 8 % (a sink of 99 % beside
-// 4096 keys), now 0.2.  Less than half a step, so a weight of 0 stays 0.
-__device__ __forceinline__ constexpr float spread(int c) {
-  const int turned = (c & 1) << 3 | (c & 2) << 1 | (c & 4) >> 1 | (c & 8) >> 3;   // neighbours far apart
-  return (static_cast<float>(turned) - 7.5f) / 16.f * (0x1p-9f / kLow);
+// Added to a weight before it is coded (RP <= 64), by its key's place: each 16 keys take 16 values spread evenly
+// over one least step of w1 around 0, in an order of their own.  So weights below that step are dropped or raised
+// to it in shares that sum to what they are.  Rounded to nearest, thousands of small weights beside a dominant one
+// (an attention sink) all went the same way, while the sum of p below the line kept them: results were off by 2 to
+// 8 % (a sink of 99 % beside 4096 keys), now 0.2.  Values are spread evenly over every second, fourth and eighth
+// key too, and the order changes from 16 keys to the next: values that recur with the key's place (one order for
+// all: 2 to 8 % off for periods of 2 to 16) do not meet it.  Less than half a step: a weight of 0 stays 0.  From
+// shared memory, 8 reads a thread and block of 64 rows: 8 sequences 95.5 -> 98.5 us, blocks of 32 rows unchanged.
+__device__ __forceinline__ float spread(int order, int c) {
+  return (static_cast<float>((5 * c & 15) ^ order) - 7.5f) / 16.f * (0x1p-9f / kLow);
 }
+__device__ __forceinline__ uint32_t spread_order(int key) { return static_cast<uint32_t>(key >> 4) * 0x9e3779b1u >> 28; }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -169,7 +172,7 @@ struct Cfg {
   static constexpr uint32_t kPTile = RP == 128 ? 3 * kPBytes : kPBytes;   // both codes' rows in one tile, or three tiles
   static constexpr uint32_t kOffRing = kPBufs * kPTile;
   static constexpr uint32_t kOffTail = kOffRing + kUnits * kUnitBytes;
-  static constexpr uint32_t kSmem = 1024 + kOffTail + kTail;
+  static constexpr uint32_t kSmem = 1024 + kOffTail + kTail + (RP == 128 ? 0 : 1024);
   static_assert(kSmem <= kSmemMax, "shared memory");
   // TMEM columns: output, scores, both codes of the queries (4 dims a column)
   static constexpr int kSBufs = D == 128 ? 2 : 1;
@@ -299,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
   float* ks_s = reinterpret_cast<float*>(tail + 5120);     // [kItems][kMaxScales]
   float* vs_s = ks_s + kItems * kMaxScales;                // < 0: page not there
   int* pg_s = reinterpret_cast<int*>(vs_s + kItems * kMaxScales);   // [kItems][kMaxPg]; < 0: not there
+  float* spread_s = reinterpret_cast<float*>(tail + kTail);         // [orders][16 keys] (RP <= 64)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(sizeof(Item) * kItems <= 512, "items");
 
@@ -676,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
     // done for all 128)
     for (int i = st; i < PB * static_cast<int>(C::kPTile) / 16; i += kSoftWarps * 32)
       reinterpret_cast<uint4*>(pbuf)[i] = make_uint4(0, 0, 0, 0);
+    if (RP < 128) spread_s[st] = spread(st >> 4, st & 15);
     named_bar(1, kSoftWarps * 32);
     pdl_wait();
     bool have_item = take(0);
@@ -875,9 +880,12 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
           if (more && half_used) {
+            float4 add;                               // of four keys
 #pragma unroll
             for (int e = 0; e < KP; e += 2) {
               const int c = part * KP + e;
+              if (RP < 128 && c % 4 == 0)
+                add = reinterpret_cast<const float4*>(spread_s)[spread_order(key0 + (c & ~15)) * 4 + c % 16 / 4];
               const float fa = f[c >> 4], vb = fmaxf(vsc[c >> 4], 0.f) * kUnit<RP>;
               const float p0 = ex2(fmaf(s[c], fa, -mref)), p1 = ex2(fmaf(s[c + 1], fa, -mref));
               l[NL > 1 ? c >> 4 : 0] += p0;
@@ -894,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) qattn_kernel(const __grid_constan
                 w1[e >> 2] = c & 2 ? __byte_perm(w1[e >> 2], c1, 0x7531) : c1;
                 w2[e >> 2] = c & 2 ? __byte_perm(w2[e >> 2], c2, 0x7531) : c2;
               } else {
-                const __half2 x = __floats2half2_rn(fmaf(p0, vb, spread(c)), fmaf(p1, vb, spread(c + 1)));
+                const __half2 x = __floats2half2_rn(fmaf(p0, vb, c & 2 ? add.z : add.x), fmaf(p1, vb, c & 2 ? add.w : add.y));
                 uint16_t c0, c1;
                 uint32_t back;
                 asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c0) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
