@@ -38,8 +38,9 @@
 // codes 930, the largest score 250, the store of P 270, the rest latency between
 // them) and 6100 with 128, DRAM 2840 with every SM at work.  So long items of few rows
 // run at the pace of DRAM (64 decodes of 1k to 16k, 16 / 8 heads, 2.29 GB: 432 to 465 us
-// on one GPU or another, 4.9 to 5.3 TB/s, the clock down to 1.45 GHz at the power limit), prompt
-// chunks at that of the softmax (256 rows over 8k, 32 / 4 heads, 2 sequences: 214 us),
+// on one GPU or another, 4.9 to 5.3 TB/s, the clock down to 1.45 GHz at the power
+// limit), prompt chunks at that of the softmax (256 rows over 8k, 32 / 4 heads, 2
+// sequences: 214 us),
 // and calls of some items a CTA also pay for the unequal shares of whole splits.  Not
 // kept: 16 softmax warps, a vote after the exponentials instead of before (3%
 // slower), a larger kLazy (1 to 4% faster, coarser small weights).
@@ -88,8 +89,8 @@ constexpr int kMaxPg = 256;                // its pages: 16384 keys / 64
 // p v_scale <= 2^kLazy; in code units times kUnit: at most 362 < 448, with RP = 128
 // 23170 (e5m2 goes to 57344).  A larger kLazy moves the reference less often, a larger
 // kUnit keeps smaller weights: the least steps are 2^-9 / (32 kLow) = 2^-18 and 2^-16 /
-// 2048 = 2^-27 of the reference.  (32 rows' weights in units of 128 and 256, kLazy 1.8
-// and 0.8: 8 sequences 96 -> 107 and 109 us, the references move more often.)
+// 2048 = 2^-27 of the reference.  (RP <= 64 in units of 128 and 256, kLazy 1.8 and 0.8:
+// 8 sequences 96 -> 107 and 109 us, the references move more often.)
 constexpr float kLazy = 3.5f;
 template <int RP>
 constexpr float kUnit = RP == 128 ? 2048.f : 32.f;
